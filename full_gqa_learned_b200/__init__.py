@@ -18,13 +18,14 @@ import threading
 from typing import Optional, Tuple
 
 __all__ = ["attn_fwd", "attn_fwd_heads", "attn_fwd_fp16", "fp16_workspace_bytes", "attn_fwd_static", "static_status", "qkv_proj", "o_proj", "attn_layer_fwd",
-           "attn_decode", "attn_bwd", "flint_attention", "workspace_bytes",
+           "attn_decode", "paged_append", "paged_read", "attn_paged", "paged_workspace_bytes", "attn_bwd", "flint_attention", "workspace_bytes",
            "decode_workspace_bytes", "bwd_workspace_bytes", "device_status", "load_library",
            "FlintError", "LIB_PATH", "HQ", "HKV", "HEAD_DIM", "STATUS", "STATIC_SCRATCH_BYTES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflint_attn.so")
 HQ, HKV, HEAD_DIM = 32, 4, 128
+PAGED_STATUS_BYTES = 256            # FLINT_PAGED_STATUS_BYTES
 STATIC_SCRATCH_BYTES = 16 << 20     # FLINT_STATIC_SCRATCH_BYTES
 STATUS = {0: "FLINT_OK", 1: "FLINT_ERR_INVALID_ARG", 2: "FLINT_ERR_UNSUPPORTED",
           3: "FLINT_ERR_CUDA", 4: "FLINT_ERR_TIMEOUT", 5: "FLINT_ERR_WORKSPACE"}
@@ -86,6 +87,14 @@ def load_library() -> ctypes.CDLL:
         lib.flint_attn_layer_fwd.restype = ctypes.c_int
         lib.flint_attn_layer_fwd.argtypes = [P, P, P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32,
                                              F32, F32, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        lib.flint_paged_append.restype = ctypes.c_int
+        lib.flint_paged_append.argtypes = [P] * 10 + [I32] * 7 + [F32, F32, P, ctypes.c_size_t, P]
+        lib.flint_paged_read.restype = ctypes.c_int
+        lib.flint_paged_read.argtypes = [P] * 7 + [I32] * 6 + [P, P, P, ctypes.c_size_t, P]
+        lib.flint_attn_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.flint_attn_paged_workspace_bytes.argtypes = [I32, I32, I32, I32]
+        lib.flint_attn_paged.restype = ctypes.c_int
+        lib.flint_attn_paged.argtypes = [P] * 10 + [I32] * 9 + [F32, F32, P, P, P, ctypes.c_size_t, P]
         lib.flint_attn_device_status.restype = ctypes.c_int
         lib.flint_attn_device_status.argtypes = [P, P]
         lib.flint_attn_last_error.restype = ctypes.c_char_p
@@ -237,6 +246,190 @@ def attn_decode(q, k, v, q_norm_w, k_norm_w, sinks, k_cache, v_cache, cache_len,
     if st != 0:
         raise FlintError(st, lib.flint_attn_last_error().decode())
     attn_decode.last_workspace = workspace
+    return out, lse
+
+
+def paged_workspace_bytes(B: int, T: int, max_new: int, kv_heads: int = HKV) -> int:
+    return int(load_library().flint_attn_paged_workspace_bytes(int(B), int(T), int(max_new), int(kv_heads)))
+
+
+def _check_on(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+
+
+def _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu):
+    """Checks what the paged calls take alike; returns (B, kv_heads, page size)."""
+    import torch
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("give k_scales and v_scales (8-bit pages) or neither (16-bit pages)")
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.shape[3] != HEAD_DIM:
+        raise ValueError("k_pages must be [num_pages, kv_heads, page_size, 128]")
+    shape = tuple(k_pages.shape)
+    if k_scales is None:
+        _check(k_pages, "k_pages", torch.float16)
+        _check(v_pages, "v_pages", torch.bfloat16, shape)
+    else:
+        _check(k_pages, "k_pages", torch.float8_e4m3fn)
+        _check(v_pages, "v_pages", torch.float8_e4m3fn, shape)
+        _check(k_scales, "k_scales", torch.float8_e8m0fnu, shape[:3])
+        _check(v_scales, "v_scales", torch.float8_e8m0fnu, shape[:3])
+    _check(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B = int(page_table.shape[0])
+    _check(start, "cache_len", torch.int32, (B,))
+    _check(cu, "cu_new", torch.int32, (B + 1,))
+    _check_on(k_pages.device, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, page_table=page_table,
+              cache_len=start, cu_new=cu)
+    return B, shape[1], shape[2]
+
+
+def _paged_stream(stream, dev, allocated):
+    """The call's stream as a number.  Tensors that the call allocated on
+    torch's current stream are kept until another stream has passed them."""
+    import torch
+    current = torch.cuda.current_stream(dev)
+    if stream is None:
+        return current.cuda_stream
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    if stream.cuda_stream != current.cuda_stream:
+        for t in allocated:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def paged_append(k, v, k_norm_w, k_pages, v_pages, page_table, cache_len, cu_new, *, k_scales=None,
+                 v_scales=None, use_rope: bool = True, rope_theta: float = 10000.0, eps: float = 1e-6,
+                 workspace=None, stream=None) -> None:
+    """Write new tokens into a paged cache (see include/flint_attn.h,
+    flint_paged_append).
+
+    k, v [T,g,128] bf16 (g = 1, 2 or 4 KV heads): the packed new tokens'
+    projections; cu_new [B+1] int32 their boundaries; sequence b's first new
+    token sits at position cache_len[b] (int32 [B]).  k_pages, v_pages
+    [P,g,ps,128] (ps 16, 32, 64 or 128) hold position p of sequence b in page
+    page_table[b, p // ps] (int32 [B,max_pages]; -1: not kept), slot p % ps.
+    16-bit pages: k_pages float16 (normalised, rotated keys), v_pages
+    bfloat16.  8-bit pages: both float8_e4m3fn, with k_scales and v_scales
+    [P,g,ps] float8_e8m0fnu.
+    """
+    import torch
+    lib = load_library()
+    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
+    dev = k_pages.device
+    T = int(k.shape[0]) if k.dim() >= 1 else 0
+    _check(k, "k", torch.bfloat16, (T, g, HEAD_DIM))
+    _check(v, "v", torch.bfloat16, (T, g, HEAD_DIM))
+    _check(k_norm_w, "k_norm_w", torch.float32, (HEAD_DIM,))
+    _check_on(dev, k=k, v=v, k_norm_w=k_norm_w)
+    own = []
+    if workspace is None:
+        workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
+        own.append(workspace)
+    _check(workspace, "workspace", torch.uint8)
+    _check_on(dev, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.flint_paged_append(
+            _ptr(k), _ptr(v), _ptr(k_norm_w), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+            _ptr(page_table), _ptr(cache_len), _ptr(cu_new), B, T, int(page_table.shape[1]),
+            int(k_pages.shape[0]), ps, g, int(bool(use_rope)), float(rope_theta), float(eps),
+            _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
+    if st != 0:
+        raise FlintError(st, lib.flint_attn_last_error().decode())
+    paged_append.last_workspace = workspace
+
+
+def paged_read(k_pages, v_pages, page_table, start, cu_out, T: int, *, k_scales=None, v_scales=None, k=None,
+               v=None, workspace=None, stream=None) -> Tuple[object, object]:
+    """Read positions back out of a paged cache (see include/flint_attn.h,
+    flint_paged_read): row cu_out[b] + i of the result is position
+    start[b] + i of sequence b.  Returns (k [T,g,128] float16: the normalised,
+    rotated keys, v [T,g,128] bfloat16); rows from cu_out[B] on are left as
+    they were (unset unless k and v are given).  Other arguments as for
+    paged_append."""
+    import torch
+    lib = load_library()
+    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu_out)
+    dev = k_pages.device
+    T = int(T)
+    if T < 0:
+        raise ValueError("T must not be negative")
+    own = []
+    if k is None:
+        k = torch.empty((T, g, HEAD_DIM), dtype=torch.float16, device=dev)
+        own.append(k)
+    if v is None:
+        v = torch.empty((T, g, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        own.append(v)
+    if workspace is None:
+        workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
+        own.append(workspace)
+    _check(k, "k", torch.float16, (T, g, HEAD_DIM))
+    _check(v, "v", torch.bfloat16, (T, g, HEAD_DIM))
+    _check(workspace, "workspace", torch.uint8)
+    _check_on(dev, k=k, v=v, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.flint_paged_read(
+            _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(start),
+            _ptr(cu_out), B, T, int(page_table.shape[1]), int(k_pages.shape[0]), ps, g, _ptr(k), _ptr(v),
+            _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
+    if st != 0:
+        raise FlintError(st, lib.flint_attn_last_error().decode())
+    paged_read.last_workspace = workspace
+    return k, v
+
+
+def attn_paged(q, q_norm_w, sinks, k_pages, v_pages, page_table, cache_len, cu_new, *, max_new: int,
+               k_scales=None, v_scales=None, window: int = 513, use_rope: bool = True,
+               rope_theta: float = 10000.0, eps: float = 1e-6, out=None, lse=None, workspace=None,
+               stream=None, want_lse: bool = True) -> Tuple[object, object]:
+    """Attention of new tokens over a paged cache (see include/flint_attn.h,
+    flint_attn_paged); their own keys are in the pages already (paged_append).
+
+    q [T,8g,128] bf16: the packed new tokens' projected queries; max_new: at
+    least the most new tokens of any sequence (a host number, so that the
+    call does not wait for the device).  One token per sequence is a decode
+    step, a few are drafted tokens, many a prompt's chunk; a call may mix
+    them.  window 0 = full causal.  Returns (out [T,8g x 128] bf16, lse
+    [8g,T] f32 or None); rows from cu_new[B] on are left as they were (unset
+    unless out and lse are given).  Other arguments as for paged_append.
+    """
+    import torch
+    lib = load_library()
+    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
+    dev = k_pages.device
+    T = int(q.shape[0]) if q.dim() >= 1 else 0
+    nh = HQ // HKV * g
+    _check(q, "q", torch.bfloat16, (T, nh, HEAD_DIM))
+    _check(q_norm_w, "q_norm_w", torch.float32, (HEAD_DIM,))
+    _check(sinks, "sinks", torch.float32, (nh,))
+    own = []
+    if out is None:
+        out = torch.empty((T, nh * HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        own.append(out)
+    if lse is None and want_lse:
+        lse = torch.empty((nh, T), dtype=torch.float32, device=dev)
+        own.append(lse)
+    if workspace is None:
+        workspace = torch.empty(max(paged_workspace_bytes(B, T, max_new, g), 256), dtype=torch.uint8, device=dev)
+        own.append(workspace)
+    _check(out, "out", torch.bfloat16, (T, nh * HEAD_DIM))
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (nh, T))
+    _check(workspace, "workspace", torch.uint8)
+    _check_on(dev, q=q, q_norm_w=q_norm_w, sinks=sinks, out=out, lse=lse, workspace=workspace)
+    with torch.cuda.device(dev):
+        st = lib.flint_attn_paged(
+            _ptr(q), _ptr(q_norm_w), _ptr(sinks), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+            _ptr(page_table), _ptr(cache_len), _ptr(cu_new), B, T, int(max_new), int(page_table.shape[1]),
+            int(k_pages.shape[0]), ps, g, int(window), int(bool(use_rope)), float(rope_theta), float(eps),
+            _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
+    if st != 0:
+        raise FlintError(st, lib.flint_attn_last_error().decode())
+    attn_paged.last_workspace = workspace
     return out, lse
 
 

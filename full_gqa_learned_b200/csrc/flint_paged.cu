@@ -1,0 +1,536 @@
+// The paged key/value cache: writing new tokens into it, reading positions
+// back out of it, and the host side of its entry points.
+//
+// Append (one warp takes four (token, KV head) rows, eight lanes each): the
+// key gets the prologue of FlintAttention.forward (NeMo AutoModel
+// "flint.layers" API page; weight-form RMSNorm, then NeoX RoPE on sliding
+// layers), in FP32 with one rounding at the end, and goes with its value to
+// the slot the page table names.  8-bit pages: with a the row's largest
+// magnitude, e is the smallest integer in [-24, 40] with a <= 448 x 2^e (448:
+// the largest E4M3 number), the codes are E4M3(x 2^-e).  A power of two makes
+// the scaling exact, so the code's rounding (half a step, 2^-4 relative) is
+// the only one, and what is read back is exact in FP16 or BF16.  An arbitrary
+// scale would not round better: E4M3 is a floating format.
+//
+// Both kernels move bytes: 512 read and 512 or 258 written per token and head
+// (append), the reverse for reading.
+#include <cuda.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cmath>
+
+#include "flint_host.cuh"
+#include "flint_paged.cuh"
+#include "sm100.cuh"
+
+namespace flint {
+
+constexpr int kPagedThreads = 256;
+
+// One block checks what the rows' warps only step over: the packed boundaries,
+// the lengths, and every page table entry the call uses.  It writes the
+// status word itself, so no launch has to clear it.  `keep_none`: the entry
+// -1 is allowed (append: the token is not kept).
+__device__ void paged_check_block(const PagedCache& c, int* status, bool keep_none) {
+    __shared__ int s_bad;
+    if (threadIdx.x == 0) s_bad = 0;
+    __syncthreads();
+    bool bad = false;
+    // threads per sequence: a power of two, so that the entries of few long
+    // sequences and those of many short ones are both read in parallel
+    int per = 1;
+    while (per < 32 && c.B * per * 2 <= kPagedThreads) per *= 2;
+    const int sub = threadIdx.x % per;
+    if (threadIdx.x == 0 && (c.cu[0] != 0 || c.cu[c.B] > c.T)) bad = true;
+    for (int b = threadIdx.x / per; b < c.B; b += kPagedThreads / per) {
+        const int a = c.cu[b], n = c.cu[b + 1] - a, L = c.len[b];
+        if (a < 0 || n < 0 || n > c.T || L < 0 || L >= FLINT_MAX_TOKENS) { bad = true; continue; }
+        if (n == 0) continue;
+        const long long end = (long long)L + n;
+        if (end > FLINT_MAX_TOKENS || end > ((long long)c.max_pages << c.ps_log2)) { bad = true; continue; }
+        const int p1 = (int)((end - 1) >> c.ps_log2);
+        for (int i = (L >> c.ps_log2) + sub; i <= p1; i += per) {
+            const int pg = c.table[(size_t)b * c.max_pages + i];
+            if (pg >= c.num_pages || pg < (keep_none ? -1 : 0)) bad = true;
+        }
+    }
+    if (bad) s_bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) *status = s_bad ? kStatusInvalid : kStatusOk;
+}
+
+// Sequence, position and pool row of packed row t (warp-uniform t); false
+// where the row belongs to no sequence or has no page.
+__device__ __forceinline__ bool paged_locate(const PagedCache& c, int t, int* pos, int* page, int* slot) {
+    const int b = warp_last_leq(c.cu, c.B, t);
+    const int a = c.cu[b], z = c.cu[b + 1], L = c.len[b];
+    if (t < a || t >= z || L < 0) return false;
+    const long long p = (long long)L + (t - a);
+    if (p >= FLINT_MAX_TOKENS || (p >> c.ps_log2) >= c.max_pages) return false;
+    *pos = (int)p;
+    *slot = (int)p & ((1 << c.ps_log2) - 1);
+    *page = c.table[(size_t)b * c.max_pages + (int)(p >> c.ps_log2)];
+    return *page >= 0 && *page < c.num_pages;
+}
+
+// E8M0 exponent e of a row whose largest magnitude is a.
+__device__ __forceinline__ int paged_exponent(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int E = (int)(u >> 23) - 127;                       // a = 1.m x 2^E
+    const int e = E - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);   // 448 = 1.75 x 2^8
+    return min(max(e, kPagedEMin), kPagedEMax);
+}
+
+// Eight values x 2^-e as E4M3 codes (round to nearest even, saturating).
+__device__ __forceinline__ uint2 paged_codes8(const float* x, float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+struct AppendParams {
+    PagedCache c;
+    const __nv_bfloat16* k;      // [T, ng, 128]
+    const __nv_bfloat16* v;
+    const float* k_norm_w;
+    void* k_pages;
+    void* v_pages;
+    uint8_t* k_scales;           // null: 16-bit pages
+    uint8_t* v_scales;
+    int* status;
+    int use_rope;
+    float rope_theta, eps;
+};
+
+template <int NG, bool FP8>
+__global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const AppendParams p) {
+    if (blockIdx.x == gridDim.x - 1) {
+        paged_check_block(p.c, p.status, true);
+        return;
+    }
+    __shared__ double s_inv[64];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = lane >> 3, sub = lane & 7;
+    if (p.use_rope) {
+        if (tid < 64) s_inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
+        __syncthreads();
+    }
+    float w0[8], w1[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        w0[e] = p.k_norm_w[8 * sub + e];
+        w1[e] = p.k_norm_w[64 + 8 * sub + e];
+    }
+    const int nrows = p.c.T * NG;                             // T <= 2^24
+    const int nw = (gridDim.x - 1) * (kPagedThreads >> 5);
+    for (int wi = blockIdx.x * (kPagedThreads >> 5) + warp; 4 * wi < nrows; wi += nw) {
+        const int r = 4 * wi + grp;
+        const bool in = r < nrows;
+        const size_t src = (size_t)(in ? r : 0) * kHD;
+        const uint4 ka = *reinterpret_cast<const uint4*>(p.k + src + 8 * sub);
+        const uint4 kb = *reinterpret_cast<const uint4*>(p.k + src + 64 + 8 * sub);
+        const uint4 va = *reinterpret_cast<const uint4*>(p.v + src + 8 * sub);
+        const uint4 vb = *reinterpret_cast<const uint4*>(p.v + src + 64 + 8 * sub);
+        // the warp's 4 / NG tokens, one search each
+        int pos = 0, page = 0, slot = 0;
+        bool ok = false;
+#pragma unroll
+        for (int i = 0; i < 4 / NG; ++i) {
+            const int t = (4 * wi) / NG + i;
+            int po = 0, pg = 0, sl = 0;
+            bool o = false;
+            if (t < p.c.T) o = paged_locate(p.c, t, &po, &pg, &sl);
+            if (grp / NG == i) { pos = po; page = pg; slot = sl; ok = o; }
+        }
+        ok = ok && in;
+        float x0[8], x1[8];
+        const uint32_t aw[4] = {ka.x, ka.y, ka.z, ka.w}, bw[4] = {kb.x, kb.y, kb.z, kb.w};
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x0[e] = (e & 1) ? __uint_as_float(aw[e >> 1] & 0xffff0000u) : __uint_as_float(aw[e >> 1] << 16);
+            x1[e] = (e & 1) ? __uint_as_float(bw[e >> 1] & 0xffff0000u) : __uint_as_float(bw[e >> 1] << 16);
+            ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+        }
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+        const float rn = 1.f / sqrtf(ss * (1.f / kHD) + p.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x0[e] = x0[e] * rn * w0[e];
+            x1[e] = x1[e] * rn * w1[e];
+        }
+        if (p.use_rope) {
+            // a token's 64 rotations are shared by its NG heads: 8 / NG each
+            // lane, exchanged by shuffles
+            constexpr int kPer = 8 / NG;
+            const int li = lane & (8 * NG - 1), base = lane & ~(8 * NG - 1);
+            float mc[kPer], ms[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) rope_cos_sin_exact(pos, s_inv[kPer * li + e], &mc[e], &ms[e]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int f = 8 * sub + e;
+                const float c = __shfl_sync(0xffffffffu, mc[e % kPer], base + f / kPer);
+                const float s = __shfl_sync(0xffffffffu, ms[e % kPer], base + f / kPer);
+                const float y0 = x0[e] * c - x1[e] * s;
+                const float y1 = x1[e] * c + x0[e] * s;
+                x0[e] = y0;
+                x1[e] = y1;
+            }
+        }
+        const size_t row = ok ? paged_row(p.c, page, r % NG, slot) : 0;
+        if constexpr (!FP8) {
+            if (ok) {
+                __half2 h[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // |k~| <= sqrt(128) max|w|: only weights above 5,789 reach the clamp
+                    h[e] = __floats2half2_rn(fminf(fmaxf(x0[2 * e], -65504.f), 65504.f),
+                                             fminf(fmaxf(x0[2 * e + 1], -65504.f), 65504.f));
+                    h[4 + e] = __floats2half2_rn(fminf(fmaxf(x1[2 * e], -65504.f), 65504.f),
+                                                 fminf(fmaxf(x1[2 * e + 1], -65504.f), 65504.f));
+                }
+                __half* kd = static_cast<__half*>(p.k_pages) + row * kHD + 8 * sub;
+                __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.v_pages) + row * kHD + 8 * sub;
+                *reinterpret_cast<uint4*>(kd) = *reinterpret_cast<uint4*>(&h[0]);
+                *reinterpret_cast<uint4*>(kd + 64) = *reinterpret_cast<uint4*>(&h[4]);
+                *reinterpret_cast<uint4*>(vd) = va;
+                *reinterpret_cast<uint4*>(vd + 64) = vb;
+            }
+        } else {
+            float y0[8], y1[8];
+            const uint32_t cw[4] = {va.x, va.y, va.z, va.w}, dw[4] = {vb.x, vb.y, vb.z, vb.w};
+            float ak = 0.f, av = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y0[e] = (e & 1) ? __uint_as_float(cw[e >> 1] & 0xffff0000u) : __uint_as_float(cw[e >> 1] << 16);
+                y1[e] = (e & 1) ? __uint_as_float(dw[e >> 1] & 0xffff0000u) : __uint_as_float(dw[e >> 1] << 16);
+                ak = fmaxf(ak, fmaxf(fabsf(x0[e]), fabsf(x1[e])));
+                av = fmaxf(av, fmaxf(fabsf(y0[e]), fabsf(y1[e])));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
+                av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
+            }
+            const int ek = paged_exponent(ak), ev = paged_exponent(av);
+            const float ik = __uint_as_float((uint32_t)(127 - ek) << 23), iv = __uint_as_float((uint32_t)(127 - ev) << 23);
+            if (ok) {
+                uint8_t* kd = static_cast<uint8_t*>(p.k_pages) + row * kHD + 8 * sub;
+                uint8_t* vd = static_cast<uint8_t*>(p.v_pages) + row * kHD + 8 * sub;
+                *reinterpret_cast<uint2*>(kd) = paged_codes8(x0, ik);
+                *reinterpret_cast<uint2*>(kd + 64) = paged_codes8(x1, ik);
+                *reinterpret_cast<uint2*>(vd) = paged_codes8(y0, iv);
+                *reinterpret_cast<uint2*>(vd + 64) = paged_codes8(y1, iv);
+                if (sub == 0) {
+                    p.k_scales[row] = (uint8_t)(ek + 127);
+                    p.v_scales[row] = (uint8_t)(ev + 127);
+                }
+            }
+        }
+    }
+}
+
+struct ReadParams {
+    PagedCache c;                // len: first position of each sequence's run
+    const void* k_pages;
+    const void* v_pages;
+    const uint8_t* k_scales;     // null: 16-bit pages
+    const uint8_t* v_scales;
+    __half* k;                   // [T, ng, 128]
+    __nv_bfloat16* v;
+    int* status;
+};
+
+__device__ __forceinline__ float2 paged_decode2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <int NG, bool FP8>
+__global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadParams p) {
+    if (blockIdx.x == gridDim.x - 1) {
+        paged_check_block(p.c, p.status, false);
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int grp = lane >> 3, sub = lane & 7;
+    const int nrows = p.c.T * NG;
+    const int nw = (gridDim.x - 1) * (kPagedThreads >> 5);
+    for (int wi = blockIdx.x * (kPagedThreads >> 5) + warp; 4 * wi < nrows; wi += nw) {
+        const int r = 4 * wi + grp;
+        int page = 0, slot = 0;
+        bool ok = false, mine = false;
+#pragma unroll
+        for (int i = 0; i < 4 / NG; ++i) {
+            const int t = (4 * wi) / NG + i;
+            int po = 0, pg = 0, sl = 0;
+            bool o = false;
+            if (t < p.c.T) o = paged_locate(p.c, t, &po, &pg, &sl);
+            if (grp / NG == i) { page = pg; slot = sl; ok = o; mine = t < p.c.cu[p.c.B]; }
+        }
+        if (r >= nrows || !mine) continue;                    // rows behind the last sequence stay as they were
+        const size_t row = ok ? paged_row(p.c, page, r % NG, slot) : 0;
+        uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;   // a row without a page reads as zeros
+        if constexpr (!FP8) {
+            if (ok) {
+                const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.k_pages) + row * kHD);
+                const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.v_pages) + row * kHD);
+                k0 = __ldg(ks + sub); k1 = __ldg(ks + 8 + sub);
+                v0 = __ldg(vs + sub); v1 = __ldg(vs + 8 + sub);
+            }
+            uint4* kd = reinterpret_cast<uint4*>(p.k + (size_t)r * kHD);
+            uint4* vd = reinterpret_cast<uint4*>(p.v + (size_t)r * kHD);
+            kd[sub] = k0; kd[8 + sub] = k1;
+            vd[sub] = v0; vd[8 + sub] = v1;
+        } else {
+            if (ok) {
+                const uint4 kc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + row * kHD) + sub);
+                const uint4 vc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + row * kHD) + sub);
+                const float sk = paged_scale(__ldg(p.k_scales + row)), sv = paged_scale(__ldg(p.v_scales + row));
+                const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+                __half2 ko[8];
+                __nv_bfloat162 vo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 a = paged_decode2((kw[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    const float2 b = paged_decode2((vw[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    ko[i] = __floats2half2_rn(a.x * sk, a.y * sk);
+                    vo[i] = __floats2bfloat162_rn(b.x * sv, b.y * sv);
+                }
+                k0 = *reinterpret_cast<uint4*>(&ko[0]); k1 = *reinterpret_cast<uint4*>(&ko[4]);
+                v0 = *reinterpret_cast<uint4*>(&vo[0]); v1 = *reinterpret_cast<uint4*>(&vo[4]);
+            }
+            uint4* kd = reinterpret_cast<uint4*>(p.k + (size_t)r * kHD + 16 * sub);
+            uint4* vd = reinterpret_cast<uint4*>(p.v + (size_t)r * kHD + 16 * sub);
+            kd[0] = k0; kd[1] = k1;
+            vd[0] = v0; vd[1] = v1;
+        }
+    }
+}
+
+// ============================================================================ host
+flint_status_t launch_paged_attn(const PagedAttnParams& p, const PagedCache& c, int sms, cudaStream_t s);
+size_t paged_attn_workspace(int B, int T, int max_new, int ng);
+
+namespace {
+
+bool al(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+struct Range {
+    explicit Range(const char* name) { nvtxRangePushA(name); }
+    ~Range() { nvtxRangePop(); }
+};
+
+// What the three entry points check alike; fills c.
+flint_status_t check_cache(PagedCache* c, const void* k_pages, const void* v_pages, const void* k_scales,
+                           const void* v_scales, const int32_t* table, const int32_t* len, const int32_t* cu,
+                           int32_t B, int32_t T, int32_t max_pages, int32_t num_pages, int32_t page_size,
+                           int32_t kv_heads) {
+    fail(FLINT_OK, "%s", "");
+    if (B < 0 || B > FLINT_MAX_DECODE_BATCH)
+        return fail(FLINT_ERR_INVALID_ARG, "B=%d outside [0, %d]", B, FLINT_MAX_DECODE_BATCH);
+    if (T < 0 || T > FLINT_MAX_TOKENS)
+        return fail(FLINT_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, FLINT_MAX_TOKENS);
+    if (kv_heads != 1 && kv_heads != 2 && kv_heads != 4)
+        return fail(FLINT_ERR_INVALID_ARG, "kv_heads=%d: 1, 2 or 4", kv_heads);
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return fail(FLINT_ERR_UNSUPPORTED, "page_size=%d: 16, 32, 64 or 128 slots", page_size);
+    if (max_pages < 1 || max_pages > FLINT_MAX_TOKENS)
+        return fail(FLINT_ERR_INVALID_ARG, "max_pages=%d outside [1, %d]", max_pages, FLINT_MAX_TOKENS);
+    if (num_pages < 1 || (long long)num_pages * kv_heads > 0x7fffffffLL)
+        return fail(FLINT_ERR_INVALID_ARG, "num_pages=%d", num_pages);
+    if ((k_scales == nullptr) != (v_scales == nullptr))
+        return fail(FLINT_ERR_INVALID_ARG, "give k_scales and v_scales (8-bit pages) or neither (16-bit pages)");
+    if (B == 0 || T == 0) return FLINT_OK;
+    if (!k_pages || !v_pages || !table || !len || !cu) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
+    if (!al(k_pages, 16) || !al(v_pages, 16) || !al(k_scales, 16) || !al(v_scales, 16))
+        return fail(FLINT_ERR_INVALID_ARG, "the pages and their scales must be 16-byte aligned");
+    if (!al(table, 4) || !al(len, 4) || !al(cu, 4)) return fail(FLINT_ERR_INVALID_ARG, "misaligned 32-bit array");
+    c->table = table;
+    c->len = len;
+    c->cu = cu;
+    c->B = B;
+    c->T = T;
+    c->max_pages = max_pages;
+    c->num_pages = num_pages;
+    c->ps_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    c->ng = kv_heads;
+    return FLINT_OK;
+}
+
+flint_status_t check_prologue(int32_t use_rope, float rope_theta, float eps) {
+    if (use_rope != 0 && use_rope != 1) return fail(FLINT_ERR_INVALID_ARG, "use_rope must be 0 or 1");
+    if (!(eps > 0.f) || !std::isfinite(eps)) return fail(FLINT_ERR_INVALID_ARG, "eps must be > 0");
+    if (use_rope && (!(rope_theta > 1.f) || !std::isfinite(rope_theta)))
+        return fail(FLINT_ERR_INVALID_ARG, "rope_theta must be > 1");
+    return FLINT_OK;
+}
+
+flint_status_t check_workspace(const void* workspace, size_t have, size_t need) {
+    if (!workspace || !al(workspace, 256))
+        return fail(FLINT_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
+    if (have < need) return fail(FLINT_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
+    return FLINT_OK;
+}
+
+// Blocks of the row kernels: a warp per four rows, at most eight blocks an SM
+// (they loop over the rest), and the checking block.
+int row_blocks(const PagedCache& c, int sms) {
+    const long long warps = ((long long)c.T * c.ng + 3) / 4;
+    long long n = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
+    if (n > 8LL * sms) n = 8LL * sms;
+    return (int)n + 1;
+}
+
+template <bool FP8>
+void launch_append(const AppendParams& p, int grid, cudaStream_t s) {
+    if (p.c.ng == 4) paged_append_kernel<4, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+    else if (p.c.ng == 2) paged_append_kernel<2, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+    else paged_append_kernel<1, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+}
+template <bool FP8>
+void launch_read(const ReadParams& p, int grid, cudaStream_t s) {
+    if (p.c.ng == 4) paged_read_kernel<4, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+    else if (p.c.ng == 2) paged_read_kernel<2, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+    else paged_read_kernel<1, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+}
+
+}  // namespace
+}  // namespace flint
+
+using namespace flint;
+
+extern "C" {
+
+flint_status_t flint_paged_append(const void* k, const void* v, const float* k_norm_w, void* k_pages,
+                                  void* v_pages, void* k_scales, void* v_scales, const int32_t* page_table,
+                                  const int32_t* cache_len, const int32_t* cu_new, int32_t B, int32_t T,
+                                  int32_t max_pages, int32_t num_pages, int32_t page_size, int32_t kv_heads,
+                                  int32_t use_rope, float rope_theta, float eps, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    Range r("flint_paged_append");
+    AppendParams p = {};
+    flint_status_t st = check_cache(&p.c, k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new, B, T,
+                                    max_pages, num_pages, page_size, kv_heads);
+    if (st == FLINT_OK) st = check_prologue(use_rope, rope_theta, eps);
+    if (st != FLINT_OK || B == 0 || T == 0) return st;
+    if (!k || !v || !k_norm_w) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
+    if (!al(k, 16) || !al(v, 16)) return fail(FLINT_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    if (!al(k_norm_w, 4)) return fail(FLINT_ERR_INVALID_ARG, "misaligned 32-bit array");
+    st = check_workspace(workspace, workspace_bytes, FLINT_PAGED_STATUS_BYTES);
+    if (st != FLINT_OK) return st;
+    int sms = 0;
+    st = device_setup(&sms);
+    if (st != FLINT_OK) return st;
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.k_norm_w = k_norm_w;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scales = static_cast<uint8_t*>(k_scales);
+    p.v_scales = static_cast<uint8_t*>(v_scales);
+    p.status = static_cast<int*>(workspace);
+    p.use_rope = use_rope;
+    p.rope_theta = rope_theta;
+    p.eps = eps;
+    const int grid = row_blocks(p.c, sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k_scales) launch_append<true>(p, grid, s);
+    else launch_append<false>(p, grid, s);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
+    return FLINT_OK;
+}
+
+flint_status_t flint_paged_read(const void* k_pages, const void* v_pages, const void* k_scales,
+                                const void* v_scales, const int32_t* page_table, const int32_t* start,
+                                const int32_t* cu_out, int32_t B, int32_t T, int32_t max_pages,
+                                int32_t num_pages, int32_t page_size, int32_t kv_heads, void* k, void* v,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    Range r("flint_paged_read");
+    ReadParams p = {};
+    flint_status_t st = check_cache(&p.c, k_pages, v_pages, k_scales, v_scales, page_table, start, cu_out, B, T,
+                                    max_pages, num_pages, page_size, kv_heads);
+    if (st != FLINT_OK || B == 0 || T == 0) return st;
+    if (!k || !v) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
+    if (!al(k, 16) || !al(v, 16)) return fail(FLINT_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    st = check_workspace(workspace, workspace_bytes, FLINT_PAGED_STATUS_BYTES);
+    if (st != FLINT_OK) return st;
+    int sms = 0;
+    st = device_setup(&sms);
+    if (st != FLINT_OK) return st;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scales = static_cast<const uint8_t*>(k_scales);
+    p.v_scales = static_cast<const uint8_t*>(v_scales);
+    p.k = static_cast<__half*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
+    p.status = static_cast<int*>(workspace);
+    const int grid = row_blocks(p.c, sms);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k_scales) launch_read<true>(p, grid, s);
+    else launch_read<false>(p, grid, s);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "read launch: %s", cudaGetErrorString(e));
+    return FLINT_OK;
+}
+
+size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new, int32_t kv_heads) {
+    if (B < 0 || B > FLINT_MAX_DECODE_BATCH || T < 0 || T > FLINT_MAX_TOKENS || max_new < 0 ||
+        (kv_heads != 1 && kv_heads != 2 && kv_heads != 4))
+        return 0;
+    return paged_attn_workspace(B, T, max_new, kv_heads);
+}
+
+flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const float* sinks, const void* k_pages,
+                                const void* v_pages, const void* k_scales, const void* v_scales,
+                                const int32_t* page_table, const int32_t* cache_len, const int32_t* cu_new,
+                                int32_t B, int32_t T, int32_t max_new, int32_t max_pages, int32_t num_pages,
+                                int32_t page_size, int32_t kv_heads, int32_t window, int32_t use_rope,
+                                float rope_theta, float eps, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    Range r("flint_attn_paged");
+    PagedCache c = {};
+    flint_status_t st = check_cache(&c, k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new, B, T,
+                                    max_pages, num_pages, page_size, kv_heads);
+    if (st == FLINT_OK) st = check_prologue(use_rope, rope_theta, eps);
+    if (st != FLINT_OK) return st;
+    if (window < 0) return fail(FLINT_ERR_INVALID_ARG, "window=%d < 0", window);
+    if (max_new < 0) return fail(FLINT_ERR_INVALID_ARG, "max_new=%d < 0", max_new);
+    if (B == 0 || T == 0) return FLINT_OK;
+    if (!q || !q_norm_w || !sinks || !out) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
+    if (!al(q, 16) || !al(out, 16)) return fail(FLINT_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    if (!al(q_norm_w, 4) || !al(sinks, 4) || !al(lse, 4)) return fail(FLINT_ERR_INVALID_ARG, "misaligned 32-bit array");
+    st = check_workspace(workspace, workspace_bytes, paged_attn_workspace(B, T, max_new, kv_heads));
+    if (st != FLINT_OK) return st;
+    int sms = 0;
+    st = device_setup(&sms);
+    if (st != FLINT_OK) return st;
+    PagedAttnParams p = {};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.q_norm_w = q_norm_w;
+    p.sinks = sinks;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scales = static_cast<const uint8_t*>(k_scales);
+    p.v_scales = static_cast<const uint8_t*>(v_scales);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.ws = static_cast<char*>(workspace);
+    p.c = c;
+    p.max_new = max_new;
+    p.window = window;
+    p.use_rope = use_rope;
+    p.rope_theta = rope_theta;
+    p.eps = eps;
+    return launch_paged_attn(p, c, sms, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

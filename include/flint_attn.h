@@ -356,6 +356,116 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The paged key/value cache of a serving step: new tokens are written into
+ * pages (flint_paged_append), positions are read back out of them
+ * (flint_paged_read), and a ragged batch of new tokens attends to them
+ * (flint_attn_paged).  The pages hold what FlintAttention.forward (NeMo
+ * AutoModel "flint.layers" API page) sees of earlier tokens: normalised,
+ * rotated keys and values.
+ *
+ * Common arguments:
+ *  k_pages, v_pages   pools [num_pages, kv_heads, page_size, 128]; page_size
+ *             16, 32, 64 or 128, 16-byte aligned.  Position p of sequence b
+ *             lives in page page_table[b][p / page_size], slot p mod
+ *             page_size.
+ *             16-bit pages (k_scales and v_scales NULL): keys FP16, values
+ *             BF16.  (A normalised key is at most sqrt(128) max|k_norm_w|, so
+ *             FP16 holds it with 3 more bits than BF16; larger ones than
+ *             65,504 saturate.)
+ *             8-bit pages: E4M3 codes, and k_scales, v_scales [num_pages,
+ *             kv_heads, page_size] E8M0 bytes (scale 2^(byte - 127)), one a
+ *             token and head: the value is code x scale.  The scale of a row
+ *             with largest magnitude a is 2^e for the smallest e in [-24, 40]
+ *             with a <= 448 x 2^e; larger values saturate.
+ *  page_table int32 [B, max_pages].
+ *  cache_len  int32 [B]: positions cached before this call's new tokens.
+ *  cu_new     int32 [B+1]: new token t, cu_new[b] <= t < cu_new[b+1], belongs
+ *             to sequence b and sits at position cache_len[b] + t - cu_new[b].
+ *             cu_new[0] = 0, non-decreasing, cu_new[B] <= T.  A sequence may
+ *             have no new token.  Rows from cu_new[B] on belong to nobody:
+ *             they are not read, and output rows there are left as they were.
+ *  B          sequences, 0 <= B <= FLINT_MAX_DECODE_BATCH;  T  rows of the
+ *             packed tensors, 0 <= T <= FLINT_MAX_TOKENS.  B == 0 or T == 0:
+ *             no-op.
+ *  kv_heads   1, 2 or 4 KV heads (a head slice, as in flint_attn_fwd_heads),
+ *             with 8 query heads each.
+ *  use_rope, rope_theta, eps   as for flint_attn_fwd.
+ *  workspace  256-byte aligned device buffer whose first word is the device
+ *             status (flint_attn_device_status): FLINT_ERR_INVALID_ARG for
+ *             ill-formed cu_new or cache_len, a position past
+ *             max_pages x page_size or FLINT_MAX_TOKENS, or a page the call
+ *             needs that is outside [0, num_pages).  Such sequences' results
+ *             are undefined; nothing outside the pools is accessed.
+ */
+#define FLINT_PAGED_STATUS_BYTES 256
+
+/*
+ * Writes the new tokens into their pages.
+ *  k, v       bf16 [T, kv_heads, 128]: projected keys (before k_norm) and
+ *             values, 16-byte aligned.
+ *  k_norm_w   fp32 [128].
+ *  workspace  FLINT_PAGED_STATUS_BYTES bytes.
+ * A page table entry of -1 drops the token (a sliding layer keeps no page
+ * for positions that no later token sees).  A slot that several tokens of one
+ * call name (a page listed twice) ends up with the rows of any of them.
+ * Infinite elements saturate in 8-bit pages; NaN stays NaN.
+ */
+FLINT_API flint_status_t flint_paged_append(const void* k, const void* v, const float* k_norm_w,
+                              void* k_pages, void* v_pages, void* k_scales, void* v_scales,
+                              const int32_t* page_table, const int32_t* cache_len,
+                              const int32_t* cu_new, int32_t B, int32_t T, int32_t max_pages,
+                              int32_t num_pages, int32_t page_size, int32_t kv_heads,
+                              int32_t use_rope, float rope_theta, float eps,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Reads cached positions back into packed rows: row t of sequence b (cu_out)
+ * is position start[b] + t - cu_out[b].
+ *  k          fp16 [T, kv_heads, 128]: keys as attention sees them.
+ *  v          bf16 [T, kv_heads, 128].  Both exact (8-bit keys with a scale
+ *             below 2^-15 are rounded to FP16's subnormals).  A row whose
+ *             page is missing is zeros.
+ *  workspace  FLINT_PAGED_STATUS_BYTES bytes.
+ */
+FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pages,
+                              const void* k_scales, const void* v_scales,
+                              const int32_t* page_table, const int32_t* start,
+                              const int32_t* cu_out, int32_t B, int32_t T, int32_t max_pages,
+                              int32_t num_pages, int32_t page_size, int32_t kv_heads,
+                              void* k, void* v, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Causal sink attention of the new tokens over their sequences' pages, the
+ * new tokens' own keys included: flint_paged_append comes first.  The token
+ * at position p sees positions max(0, p - window + 1) .. p (window > 0) or
+ * 0 .. p (window == 0), and the sink.  One new token a sequence is a decode
+ * step, a few are drafted tokens under verification, many a prompt's chunk;
+ * one call may mix them.
+ *  q          bf16 [T, 8 kv_heads, 128]: projected queries, before q_norm.
+ *  q_norm_w   fp32 [128];  sinks  fp32 [8 kv_heads].
+ *  max_new    at least the most new tokens of any sequence (else the device
+ *             status becomes FLINT_ERR_INVALID_ARG); chooses the kernels.
+ *  out        bf16 [T, 8 kv_heads x 128];  lse  fp32 [8 kv_heads, T] or NULL.
+ *  workspace  flint_attn_paged_workspace_bytes(B, T, max_new, kv_heads)
+ *             bytes; not shared by calls that may overlap on the GPU.
+ * Cached values and keys at positions a token sees must be finite and scales
+ * within 2^-24 .. 2^40; slots of other positions may hold anything, and page
+ * table entries that no new token's window touches are not read.
+ * Results do not depend on timing: every sum has a fixed order.
+ */
+FLINT_API size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new,
+                              int32_t kv_heads);
+FLINT_API flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const float* sinks,
+                              const void* k_pages, const void* v_pages, const void* k_scales,
+                              const void* v_scales, const int32_t* page_table,
+                              const int32_t* cache_len, const int32_t* cu_new, int32_t B,
+                              int32_t T, int32_t max_new, int32_t max_pages, int32_t num_pages,
+                              int32_t page_size, int32_t kv_heads, int32_t window,
+                              int32_t use_rope, float rope_theta, float eps, void* out,
+                              float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Gradient of flint_attn_fwd.  The "flint" model page (NeMo AutoModel,
  * "Parallelism and backends") makes every head's sink a trainable FP32
  * parameter whose adjoint needs care; the call computes the exact derivative
