@@ -95,39 +95,130 @@ struct PagedAttnParams {
     char* ws;
     PagedCache c;
     int max_new, window, use_rope;
-    int ctas;                    // CTAs of the step kernel
+    int step_ctas, chunk_ctas;   // CTAs of the two kernels (chunk: 0 where it is not run)
     float rope_theta, eps;
 };
 
-// A row group of the step kernel: up to NT consecutive new tokens of one
-// sequence; its tiles are runs of positions from the 16-aligned start of what
-// its rows see.
+// A row group: consecutive new tokens of one sequence that a kernel takes
+// together (at most `nt` of its list).  Its tiles are runs of positions from
+// the aligned start of what its rows see.
 struct PagedGroup { int b, row0, nrows, tiles; };
+
+// The work of one kernel: the tiles of all (group, KV head) pairs in a row,
+// group by group, head by head.  The plan kernel writes the groups and the
+// exclusive prefix of their tile counts (prefix[n] = tiles); CTA c of G takes
+// tiles [W c / G, W (c + 1) / G) of the W = tiles x heads, so every CTA has
+// the same number for any mix of lengths, and holds at most two pairs in part.
+struct PagedList { long long tiles; int n, pad; };
 
 struct PagedPlanHeader {
     int status;                  // device-side status (0 = ok)
-    int n_groups;                // row groups of the step kernel
-    long long tiles;             // the sum of their tiles (of one KV head)
-    int pad[60];
+    int pad0;
+    PagedList step, chunk;
+    int pad[54];
 };
 static_assert(sizeof(PagedPlanHeader) == 256, "plan header");
 
-// Workspace of an attention call.
+// What the plan kernel needs to know of a list: sequences of n_min .. n_max
+// new tokens, in groups of nt, whose tiles start at a multiple of align.
+struct PagedListSpec { int n_min, n_max, nt, tile, align; };
+
+constexpr int kChunkTok = 32;            // new tokens of a chunk kernel's group
+constexpr int kPagedStepRows = 16;       // query rows of a step partial
+// floats of a step partial: m[16], l[16], O[16][128]; of a chunk partial:
+// m[256], l[256], O[32][256][4] (channel quads outermost)
+constexpr size_t kStepPart = (size_t)kPagedStepRows * (kHD + 2);
+constexpr size_t kChunkPart = (size_t)8 * kChunkTok * (kHD + 2);
+
+// Workspace of an attention call.  sms: CTAs of the chunk kernel (0: not run).
 struct PagedWs {
-    size_t header, inv, groups, prefix, arrive, part, total;
+    size_t header, inv, sgroups, sprefix, arrive, spart, cgroups, cprefix, cpart, total;
 };
-__host__ __device__ inline PagedWs paged_ws(int T, int ng, int ctas) {
+__host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas, int chunk_ctas) {
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.inv = o;    o += 64 * sizeof(double);
-    L.groups = o; o = ws_align(o + sizeof(PagedGroup) * (size_t)T, 256);
-    L.prefix = o; o = ws_align(o + sizeof(long long) * ((size_t)T + 1), 256);
-    L.arrive = o; o = ws_align(o + sizeof(int) * (size_t)T * ng, 256);
-    // two partials a CTA (its first and its last segment), up to 16 rows each
-    L.part = o;   o = ws_align(o + sizeof(float) * (size_t)ctas * 2 * 16 * (kHD + 2), 256);
+    L.inv = o;     o += 64 * sizeof(double);
+    L.sgroups = o; o = ws_align(o + sizeof(PagedGroup) * (size_t)T, 256);
+    L.sprefix = o; o = ws_align(o + sizeof(long long) * ((size_t)T + 1), 256);
+    L.arrive = o;  o = ws_align(o + sizeof(int) * (size_t)T * ng, 256);
+    L.spart = o;   o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
+    L.cgroups = L.cprefix = L.cpart = o;
+    if (chunk_ctas > 0) {
+        const size_t n = (size_t)T / kChunkTok + (B < T ? B : T);
+        L.cgroups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
+        L.cprefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
+        L.cpart = o;   o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
+    }
     L.total = o;
     return L;
+}
+
+// Joins the sink to a row's running state (M, L in log2 units, O in units of
+// 2^M): the output is O x *scale.
+__device__ __forceinline__ void paged_finish(float M, float L, float sink, float* scale, float* lse) {
+    if (sink == INFINITY) {
+        *scale = 0.f;
+        *lse = INFINITY;
+        return;
+    }
+    const float s2 = sink * 1.4426950408889634f;
+    const float m = fmaxf(M, s2);
+    const float a = M > -INFINITY ? exp2f(M - m) : 0.f;
+    const float l = L * a + (s2 > -INFINITY ? exp2f(s2 - m) : 0.f);
+    *scale = l > 0.f ? a / l : 0.f;
+    *lse = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+}
+
+// One (group, head) pair's part of a CTA's share.
+struct PagedShare {
+    const PagedGroup* groups;
+    const long long* prefix;
+    long long W, G;              // tiles of all pairs, CTAs that share them
+    long long t, t_begin, t_end; // the CTA's share; t: next tile
+    int gi, head, ng;
+};
+struct PagedSeg {
+    PagedGroup g;
+    long long seg;               // the pair's first tile, of all W
+    int gi, head, t0, t1;        // this CTA's tiles [t0, t1) of the pair
+    bool whole, first;           // all of it; the CTA's first pair
+};
+__device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedList& l, const PagedGroup* groups,
+                                                  const long long* prefix, int ng, int cta, int ctas) {
+    s.groups = groups;
+    s.prefix = prefix;
+    s.ng = ng;
+    s.W = l.tiles * ng;
+    s.G = s.W < (long long)ctas ? s.W : (long long)ctas;
+    if (cta >= s.G) return false;
+    s.t = s.t_begin = s.W * cta / s.G;
+    s.t_end = s.W * (cta + 1) / s.G;
+    s.gi = warp_last_leq(prefix, l.n, s.t / ng);
+    s.head = (int)((s.t - prefix[s.gi] * ng) / groups[s.gi].tiles);
+    return true;
+}
+__device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g) {
+    if (s.t >= s.t_end) return false;
+    if (s.head == s.ng) { s.head = 0; ++s.gi; }
+    g.g = s.groups[s.gi];
+    g.gi = s.gi;
+    g.head = s.head;
+    g.seg = s.prefix[s.gi] * s.ng + (long long)s.head * g.g.tiles;
+    g.t0 = (int)(s.t - g.seg);
+    g.t1 = (int)(g.g.tiles < s.t_end - g.seg ? (long long)g.g.tiles : s.t_end - g.seg);
+    g.whole = g.t0 == 0 && g.t1 == g.g.tiles;
+    g.first = s.t == s.t_begin;
+    s.t += g.t1 - g.t0;
+    ++s.head;
+    return true;
+}
+// The CTA that owns tile x.
+__device__ __forceinline__ long long paged_owner(long long W, long long G, long long x) { return ((x + 1) * G - 1) / W; }
+// The partial that CTA `cta` leaves of the pair that starts at tile seg: 2 c
+// where it is the CTA's first pair, else 2 c + 1.
+__device__ __forceinline__ size_t paged_slot(long long W, long long G, long long seg, long long cta) {
+    return 2 * (size_t)cta + (W * cta / G < seg ? 1 : 0);
 }
 
 }  // namespace flint

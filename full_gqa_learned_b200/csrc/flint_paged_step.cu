@@ -49,6 +49,8 @@
 
 namespace flint {
 
+flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s);
+
 constexpr int kStepThreads = 128;
 constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kStepStages = 3;
@@ -60,92 +62,141 @@ constexpr int kPlanThreads = 1024;
 template <bool FP8> struct StepTile { static constexpr int block = FP8 ? 32 : 16, tile = block * kStepWarps; };
 
 // ---------------------------------------------------------------- plan
-// One block: checks the boundaries and lengths, writes the row groups with
-// the exclusive prefix of their tile counts, clears the arrival counters and
-// leaves the rotation frequencies.
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p, int nt, int tile) {
-    griddep_launch_dependents();
-    __shared__ int s_bad;
-    __shared__ int s_wg[32];
-    __shared__ long long s_wt[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Exclusive prefix of v over the block; the block's total in *total.
+template <typename I>
+__device__ __forceinline__ I plan_scan(I v, I* sh, I* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    I x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        I w = sh[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const I y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        sh[lane] = w;
+    }
+    __syncthreads();
+    const I r = x - v + (warp ? sh[warp - 1] : 0);
+    *total = sh[31];
+    __syncthreads();
+    return r;
+}
+
+// Sequence b's new tokens; 0 (and *bad) where its entries are ill-formed.
+__device__ __forceinline__ int plan_new(const PagedAttnParams& p, int b, bool* bad) {
     const PagedCache& c = p.c;
-    const PagedWs L = paged_ws(c.T, c.ng, p.ctas);
+    const int a = c.cu[b], z = c.cu[b + 1], len = c.len[b], n = z - a;
+    bool ok = a >= 0 && z >= a && z <= c.T && n <= p.max_new && len >= 0 && len < FLINT_MAX_TOKENS;
+    if (ok && n > 0) {
+        const long long end = (long long)len + n;
+        ok = end <= FLINT_MAX_TOKENS && end <= ((long long)c.max_pages << c.ps_log2);
+    }
+    if (!ok) *bad = true;
+    return ok ? n : 0;
+}
+
+// Groups of one list, from the group offsets of its sequences (first[b],
+// kept in `off`: shared memory up to kPlanSeqs sequences).
+constexpr int kPlanSeqs = 4096;
+__device__ void plan_list(const PagedAttnParams& p, const PagedListSpec& q, PagedGroup* groups, long long* prefix,
+                          int* arrive, PagedList* out, int* off, int* s_bad, int* sh_i, long long* sh_l) {
+    const PagedCache& c = p.c;
+    const int tid = threadIdx.x;
+    // group offsets; past kPlanSeqs sequences the table is a sparse one (every
+    // `every`-th sequence) and the rest is walked
+    const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
+    int n_groups = 0;
+    for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
+        const int b1 = b0 + tid * every;
+        int cnt = 0;
+        bool bad = false;
+        for (int b = b1; b < min(b1 + every, c.B); ++b) {
+            const int n = plan_new(p, b, &bad);
+            if (n >= q.n_min && n <= q.n_max) cnt += (n + q.nt - 1) / q.nt;
+        }
+        if (bad) *s_bad = 1;
+        int tot;
+        const int ex = plan_scan(cnt, sh_i, &tot);
+        if (b1 < c.B) off[b1 / every] = n_groups + ex;
+        n_groups += tot;
+    }
+    __syncthreads();
+    const int n_off = (c.B + every - 1) / every;
+    long long tiles = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+        const int g = g0 + tid;
+        PagedGroup r = {0, 0, 0, 0};
+        if (g < n_groups) {
+            int lo = 0, hi = n_off - 1;                       // last entry with off <= g
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (off[mid] <= g) lo = mid; else hi = mid - 1;
+            }
+            int at = off[lo], b = lo * every;
+            bool bad = false;
+            for (;; ++b) {                                    // one step where every == 1
+                const int n = plan_new(p, b, &bad);
+                const int k = n >= q.n_min && n <= q.n_max ? (n + q.nt - 1) / q.nt : 0;
+                if (g < at + k || b == c.B - 1) {
+                    r.b = b;
+                    r.row0 = (g - at) * q.nt;
+                    r.nrows = min(q.nt, n - r.row0);
+                    const int p0 = c.len[b] + r.row0;
+                    const int first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+                    r.tiles = (p0 + r.nrows - (first & ~(q.align - 1)) + q.tile - 1) / q.tile;
+                    break;
+                }
+                at += k;
+            }
+        }
+        long long tot;
+        const long long ex = plan_scan((long long)r.tiles, sh_l, &tot);
+        if (g < n_groups) {
+            groups[g] = r;
+            prefix[g] = tiles + ex;
+            if (arrive)
+                for (int h = 0; h < c.ng; ++h) arrive[(size_t)g * c.ng + h] = 0;
+        }
+        tiles += tot;
+    }
+    if (tid == 0) {
+        prefix[n_groups] = tiles;
+        out->n = n_groups;
+        out->tiles = tiles;
+    }
+    __syncthreads();
+}
+
+// One block: checks the boundaries and lengths, writes the lists of the step
+// and the chunk kernel (chunk_ctas > 0), clears the step kernel's arrival
+// counters and leaves the rotation frequencies.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p, const PagedListSpec step,
+                                                                  const PagedListSpec chunk) {
+    griddep_launch_dependents();
+    __shared__ int s_bad, s_i[32], s_off[kPlanSeqs];
+    __shared__ long long s_l[32];
+    const int tid = threadIdx.x;
+    const PagedCache& c = p.c;
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
     double* inv = reinterpret_cast<double*>(p.ws + L.inv);
-    PagedGroup* groups = reinterpret_cast<PagedGroup*>(p.ws + L.groups);
-    long long* prefix = reinterpret_cast<long long*>(p.ws + L.prefix);
-    int* arrive = reinterpret_cast<int*>(p.ws + L.arrive);
     if (tid == 0) s_bad = (c.cu[0] != 0 || c.cu[c.B] > c.T) ? 1 : 0;
     if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     __syncthreads();
-    int run_g = 0;
-    long long run_t = 0;
-    for (int b0 = 0; b0 < c.B; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int n = 0, len = 0, ng_b = 0;
-        long long nt_b = 0;
-        auto tiles_of = [&](int row0, int nr) -> int {
-            const int p0 = len + row0;
-            const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-            return (p0 + nr - (lo & ~15) + tile - 1) / tile;
-        };
-        if (b < c.B) {
-            const int a = c.cu[b], z = c.cu[b + 1];
-            len = c.len[b];
-            n = z - a;
-            bool bad = a < 0 || z < a || z > c.T || n > p.max_new || len < 0 || len >= FLINT_MAX_TOKENS;
-            if (!bad && n > 0) {
-                const long long end = (long long)len + n;
-                bad = end > FLINT_MAX_TOKENS || end > ((long long)c.max_pages << c.ps_log2);
-            }
-            if (bad) { n = 0; s_bad = 1; }
-            ng_b = (n + nt - 1) / nt;
-            for (int r = 0; r < n; r += nt) nt_b += tiles_of(r, min(nt, n - r));
-        }
-        // exclusive prefixes over the block's sequences
-        int ig = ng_b;
-        long long it = nt_b;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int g2 = __shfl_up_sync(0xffffffffu, ig, o);
-            const long long t2 = __shfl_up_sync(0xffffffffu, it, o);
-            if (lane >= o) { ig += g2; it += t2; }
-        }
-        if (lane == 31) { s_wg[warp] = ig; s_wt[warp] = it; }
-        __syncthreads();
-        if (warp == 0) {
-            int g = s_wg[lane];
-            long long t = s_wt[lane];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int g2 = __shfl_up_sync(0xffffffffu, g, o);
-                const long long t2 = __shfl_up_sync(0xffffffffu, t, o);
-                if (lane >= o) { g += g2; t += t2; }
-            }
-            s_wg[lane] = g;
-            s_wt[lane] = t;
-        }
-        __syncthreads();
-        int gi = run_g + ig - ng_b + (warp ? s_wg[warp - 1] : 0);
-        long long ti = run_t + it - nt_b + (warp ? s_wt[warp - 1] : 0);
-        for (int r = 0; r < n; r += nt, ++gi) {
-            const int nr = min(nt, n - r), tl = tiles_of(r, nr);
-            groups[gi] = PagedGroup{b, r, nr, tl};
-            prefix[gi] = ti;
-            for (int g = 0; g < c.ng; ++g) arrive[(size_t)gi * c.ng + g] = 0;
-            ti += tl;
-        }
-        run_g += s_wg[31];
-        run_t += s_wt[31];
-        __syncthreads();
-    }
-    if (tid == 0) {
-        prefix[run_g] = run_t;
-        hdr->status = s_bad ? kStatusInvalid : kStatusOk;
-        hdr->n_groups = run_g;
-        hdr->tiles = run_t;
-    }
+    plan_list(p, step, reinterpret_cast<PagedGroup*>(p.ws + L.sgroups), reinterpret_cast<long long*>(p.ws + L.sprefix),
+              reinterpret_cast<int*>(p.ws + L.arrive), &hdr->step, s_off, &s_bad, s_i, s_l);
+    if (p.chunk_ctas > 0)
+        plan_list(p, chunk, reinterpret_cast<PagedGroup*>(p.ws + L.cgroups),
+                  reinterpret_cast<long long*>(p.ws + L.cprefix), nullptr, &hdr->chunk, s_off, &s_bad, s_i, s_l);
+    if (tid == 0) hdr->status = s_bad ? kStatusInvalid : kStatusOk;
 }
 
 // ---------------------------------------------------------------- step kernel
@@ -215,21 +266,6 @@ struct StepSmem {
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
 
-// Finishes a row: `o` the unnormalised sum in units of 2^M, L its l; the sink
-// joins as one more term.
-__device__ __forceinline__ float step_finish(float o, float M, float L, float sink, float* lse) {
-    const float s2 = sink * 1.4426950408889634f;
-    if (sink == INFINITY) {
-        *lse = INFINITY;
-        return 0.f;
-    }
-    const float m = fmaxf(M, s2);
-    const float a = M > -INFINITY ? exp2f(M - m) : 0.f;
-    const float l = L * a + (s2 > -INFINITY ? exp2f(s2 - m) : 0.f);
-    *lse = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
-    return l > 0.f ? o * a / l : 0.f;
-}
-
 template <int NT, bool FP8>
 __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kernel(const PagedAttnParams p) {
     using S = StepSmem<NT>;
@@ -241,13 +277,10 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const int j = lane >> 2, i = lane & 3;
     const PagedCache& c = p.c;
     const int ng = c.ng, nh = kGroup * ng;
-    const PagedWs L = paged_ws(c.T, ng, p.ctas);
+    const PagedWs L = paged_ws(c.B, c.T, ng, p.step_ctas, p.chunk_ctas);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
-    const PagedGroup* groups = reinterpret_cast<const PagedGroup*>(p.ws + L.groups);
-    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.prefix);
     int* arrive = reinterpret_cast<int*>(p.ws + L.arrive);
-    float* part = reinterpret_cast<float*>(p.ws + L.part);
-    constexpr size_t kPart = (size_t)16 * (kHD + 2);     // floats of a partial: m[16], l[16], O[rows][128]
+    float* part = reinterpret_cast<float*>(p.ws + L.spart);
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
     float* s_M = reinterpret_cast<float*>(smem + S::fin);
@@ -260,14 +293,10 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const float qscale = ldexpf(1.f, eq);
     griddep_wait();
 
-    const long long W = hdr->tiles * ng;
-    if (W == 0) return;
-    const long long G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
-    const long long cta = blockIdx.x;
-    if (cta >= G) return;
-    long long t = W * cta / G;
-    const long long t_begin = t, t_end = W * (cta + 1) / G;
-    int gi = warp_last_leq(prefix, hdr->n_groups, t / ng);
+    PagedShare share;
+    if (!paged_share_begin(share, hdr->step, reinterpret_cast<const PagedGroup*>(p.ws + L.sgroups),
+                           reinterpret_cast<const long long*>(p.ws + L.sprefix), ng, blockIdx.x, gridDim.x))
+        return;
 
     const uint32_t ring = sb + S::ring + warp * (kStepStages * kStepStageBytes) + lane * 16;
     const uint32_t srow = sb + S::scales + warp * (kStepStages * 64);
@@ -276,489 +305,473 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     constexpr int kRowBytes = FP8 ? kHD : 2 * kHD;
     const int slot_mask = (1 << c.ps_log2) - 1;
 
-    for (; t < t_end; ++gi) {
-        const PagedGroup grp = groups[gi];
-        const long long base = prefix[gi] * ng;
-        int head = (int)((t - base) / grp.tiles);
-        for (; head < ng && t < t_end; ++head) {
-            // ------------------------------------------------ a segment: tiles [t0, t1) of (group, head)
-            const long long seg = base + (long long)head * grp.tiles;
-            const int t0 = (int)(t - seg);
-            const int t1 = (int)min((long long)grp.tiles, t_end - seg);
-            const long long t_first = t;
-            t += t1 - t0;
-            const int len = c.len[grp.b], row_b = c.cu[grp.b];
-            const int p0 = len + grp.row0;                   // position of the group's first row
-            const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-            const int hi = p0 + grp.nrows;                   // one past the last key any row sees
-            const int key_base = (lo & ~15) + warp * TL::block;
-            const int* table = c.table + (size_t)grp.b * c.max_pages;
+    PagedSeg sg;
+    while (paged_share_next(share, sg)) {
+        const PagedGroup& grp = sg.g;
+        const int head = sg.head, t0 = sg.t0, t1 = sg.t1;
+        const int len = c.len[grp.b], row_b = c.cu[grp.b];
+        const int p0 = len + grp.row0;                   // position of the group's first row
+        const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+        const int hi = p0 + grp.nrows;                   // one past the last key any row sees
+        const int key_base = (lo & ~15) + warp * TL::block;
+        const int* table = c.table + (size_t)grp.b * c.max_pages;
 
-            // Page of a 16-position part; -1 where none of it is needed.
-            auto page_of = [&](int key) -> int {
-                return key < hi && key + 16 > lo ? __ldg(table + (key >> c.ps_log2)) : -1;
-            };
-            auto issue = [&](int tile, int stage, const int* pg) {
-                const uint32_t dst = ring + stage * kStepStageBytes;
+        // Page of a 16-position part; -1 where none of it is needed.
+        auto page_of = [&](int key) -> int {
+            return key < hi && key + 16 > lo ? __ldg(table + (key >> c.ps_log2)) : -1;
+        };
+        auto issue = [&](int tile, int stage, const int* pg) {
+            const uint32_t dst = ring + stage * kStepStageBytes;
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    const int key = key_base + tile * TL::tile + 16 * u;
-                    int page = pg[u];
-                    if (page < 0 || page >= c.num_pages) {
-                        if (key < hi && key + 16 > lo && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
-                        page = -1;
-                    }
-                    const bool live = page >= 0;
-                    const size_t row = live ? paged_row(c, page, head, key & slot_mask) : 0;
-                    // rows outside [lo, hi) are not read: their slots may hold anything
-                    auto on = [&](int r) { return live && key + r >= lo && key + r < hi; };
-                    const uint8_t* kr = kp + row * kRowBytes;
-                    const uint8_t* vr = vp + row * kRowBytes;
-                    if constexpr (!FP8) {
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int r = j + (x >> 2) * 8;
-                            cp16(dst + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 3) * 4 + i) * 16 : 0), on(r));
-                        }
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const int r = 2 * i + (x & 1) + ((x >> 1) & 1) * 8;
-                            cp16(dst + 4096 + x * 512, vr + (on(r) ? r * kRowBytes + (x >> 2) * 128 + j * 16 : 0), on(r));
-                        }
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int r = j + (x >> 1) * 8;
-                            cp16(dst + u * 4096 + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 1) * 4 + i) * 16 : 0), on(r));
-                        }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int r = 2 * i + (x & 1) + (x >> 1) * 8;
-                            cp16(dst + u * 4096 + 2048 + x * 512, vr + (on(r) ? r * kRowBytes + j * 16 : 0), on(r));
-                        }
-                        if (lane < 2) cp16(srow + stage * 64 + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + row, live);
-                    }
+            for (int u = 0; u < kSub; ++u) {
+                const int key = key_base + tile * TL::tile + 16 * u;
+                int page = pg[u];
+                if (page < 0 || page >= c.num_pages) {
+                    if (key < hi && key + 16 > lo && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
+                    page = -1;
                 }
-                cp_commit();
-            };
-            int pg[kSub];
-            const int n_it = t1 - t0;
-            // the first stages on their way before the queries
-#pragma unroll
-            for (int s = 0; s < kStepStages - 1; ++s) {
-                if (s < n_it) {
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + s) * TL::tile + 16 * u);
-                    issue(t0 + s, s, pg);
-                } else {
-                    cp_commit();
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + kStepStages - 1) * TL::tile + 16 * u);
-
-            // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
-            if (warp < 2 * NT) {
-                const int nt = warp >> 1, sub = lane & 7, hh = 4 * (warp & 1) + (lane >> 3);
-                const bool have = nt < grp.nrows;
-                const int pos = p0 + (have ? nt : 0);
-                const __nv_bfloat16* src =
-                    p.q + ((size_t)(row_b + grp.row0 + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
-                const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * sub);
-                const uint4 b = *reinterpret_cast<const uint4*>(src + 64 + 8 * sub);
-                float x0[8], x1[8], ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t aw = reg4(a, e >> 1), bw = reg4(b, e >> 1);
-                    x0[e] = (e & 1) ? __uint_as_float(aw & 0xffff0000u) : __uint_as_float(aw << 16);
-                    x1[e] = (e & 1) ? __uint_as_float(bw & 0xffff0000u) : __uint_as_float(bw << 16);
-                    ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
-                }
-                ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-                ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-                ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-                const float rn = qscale / sqrtf(ss * (1.f / kHD) + p.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x0[e] *= rn * p.q_norm_w[8 * sub + e];
-                    x1[e] *= rn * p.q_norm_w[64 + 8 * sub + e];
-                }
-                if (p.use_rope) {
-                    const double* inv = reinterpret_cast<const double*>(p.ws + L.inv);
-                    float c0, s0, c1, s1;
-                    rope_cos_sin_exact(pos, inv[2 * lane], &c0, &s0);
-                    rope_cos_sin_exact(pos, inv[2 * lane + 1], &c1, &s1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int f = 8 * sub + e;
-                        const float cc = __shfl_sync(0xffffffffu, (e & 1) ? c1 : c0, f >> 1);
-                        const float sn = __shfl_sync(0xffffffffu, (e & 1) ? s1 : s0, f >> 1);
-                        const float y0 = x0[e] * cc - x1[e] * sn, y1 = x1[e] * cc + x0[e] * sn;
-                        x0[e] = y0;
-                        x1[e] = y1;
-                    }
-                }
-                __half* qh = reinterpret_cast<__half*>(smem + S::q) + (nt * kGroup + hh) * kHD + 8 * sub;
-                __half* ql = qh + S::rows * kHD;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (!have) x0[e] = x1[e] = 0.f;
-                    const __half h0 = __float2half_rn(x0[e]), h1 = __float2half_rn(x1[e]);
-                    qh[e] = h0;
-                    qh[64 + e] = h1;
-                    ql[e] = __float2half_rn(x0[e] - __half2float(h0));
-                    ql[64 + e] = __float2half_rn(x1[e] - __half2float(h1));
-                }
-            }
-            __syncthreads();
-            // B fragments of q~ (head j, the lane's channels): [high, low][NT][16]
-            uint32_t qf[2][NT][16];
-#pragma unroll
-            for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        // 16-bit: chunk 4 x + i of 8 channels; 8-bit: the x % 2 half of chunk 4 (x / 2) + i of 16
-                        const int ch = FP8 ? ((x >> 1) * 4 + i) * 16 + (x & 1) * 8 : (x * 4 + i) * 8;
-                        const uint4 v = lds16(sb + S::q + ((pt * S::rows + nt * kGroup + j) * kHD + ch) * 2);
-                        qf[pt][nt][4 * x] = v.x;
-                        qf[pt][nt][4 * x + 1] = v.y;
-                        qf[pt][nt][4 * x + 2] = v.z;
-                        qf[pt][nt][4 * x + 3] = v.w;
-                    }
-
-            // ---- the stream
-            float acc[NT][8][4], m[NT][2], l[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int x = 0; x < 8; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
-                m[nt][0] = m[nt][1] = -INFINITY;
-                l[nt][0] = l[nt][1] = 0.f;
-            }
-            int stage = 0;
-            for (int it = 0; it < n_it; ++it) {
-                // the stage after next, into the buffer read in the last iteration
-                if (it + kStepStages - 1 < n_it) {
-                    int st2 = stage + kStepStages - 1;
-                    if (st2 >= kStepStages) st2 -= kStepStages;
-                    issue(t0 + it + kStepStages - 1, st2, pg);
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + it + kStepStages) * TL::tile + 16 * u);
-                } else {
-                    cp_commit();
-                }
-                cp_wait<kStepStages - 1>();
-                if (FP8) __syncwarp();                        // the scales were fetched by other lanes
-                const uint32_t src = ring + stage * kStepStageBytes;
-                const int key0 = key_base + (t0 + it) * TL::tile;
-                if (key0 < hi && key0 + TL::block > lo) {
-                    // scores: s[u][nt][0..3] = (key j, heads 2i, 2i + 1), (key j + 8, the same)
-                    float s[kSub][NT][4];
-                    float ev[kSub][2];
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) {
-                        float sl[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[u][nt][e] = sl[nt][e] = 0.f;
-                        if constexpr (!FP8) {
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint4 a = lds16(src + x * 512), b = lds16(src + (4 + x) * 512);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma_f16(s[u][nt], a.x, b.x, a.y, b.y, qf[0][nt][4 * x], qf[0][nt][4 * x + 1]);
-                                    mma_f16(sl[nt], a.x, b.x, a.y, b.y, qf[1][nt][4 * x], qf[1][nt][4 * x + 1]);
-                                    mma_f16(s[u][nt], a.z, b.z, a.w, b.w, qf[0][nt][4 * x + 2], qf[0][nt][4 * x + 3]);
-                                    mma_f16(sl[nt], a.z, b.z, a.w, b.w, qf[1][nt][4 * x + 2], qf[1][nt][4 * x + 3]);
-                                }
-                            }
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) s[u][nt][e] = (s[u][nt][e] + sl[nt][e]) * C;
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint4 a = lds16(src + u * 4096 + x * 512), b = lds16(src + u * 4096 + (2 + x) * 512);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const uint32_t aw = reg4(a, r), bw = reg4(b, r);
-                                    const uint32_t a0 = e4m3_f16(aw & 0xffffu), a2 = e4m3_f16(aw >> 16);
-                                    const uint32_t a1 = e4m3_f16(bw & 0xffffu), a3 = e4m3_f16(bw >> 16);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        const int f = 8 * x + 2 * r;
-                                        mma_f16(s[u][nt], a0, a1, a2, a3, qf[0][nt][f], qf[0][nt][f + 1]);
-                                        mma_f16(sl[nt], a0, a1, a2, a3, qf[1][nt][f], qf[1][nt][f + 1]);
-                                    }
-                                }
-                            }
-                            const uint8_t* ssc = smem + S::scales + (warp * kStepStages + stage) * 64 + u * 32;
-                            const float k0 = paged_scale(ssc[j]) * C, k1 = paged_scale(ssc[j + 8]) * C;
-                            ev[u][0] = (float)((int)ssc[16 + j] - 127);
-                            ev[u][1] = (float)((int)ssc[24 + j] - 127);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    s[u][nt][e] = fmaf(s[u][nt][e] + sl[nt][e], e < 2 ? k0 : k1, ev[u][e >> 1]);
-                        }
-                    }
-                    // masks: only where some row does not see the whole block
-                    if (key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window)) {
-#pragma unroll
-                        for (int u = 0; u < kSub; ++u) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const int pos = p0 + nt, wl = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int k = key0 + 16 * u + j + (e >> 1) * 8;
-                                    if (k > pos || k < wl) s[u][nt][e] = -INFINITY;
-                                }
-                            }
-                            // slots that hold no key of this call have any scale
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int k = key0 + 16 * u + j + 8 * e;
-                                if (k < lo || k >= hi) ev[u][e] = 0.f;
-                            }
-                        }
-                    }
-                    // raise the running max where a score passes it by 2^8
-                    bool up = false;
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) up = up || s[u][nt][e] > m[nt][e & 1] + 8.f;
-                    if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float mx = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
-                                if (kSub == 2) mx = fmaxf(mx, fmaxf(s[kSub - 1][nt][h], s[kSub - 1][nt][2 + h]));
-#pragma unroll
-                                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                                const float mn = fmaxf(m[nt][h], mx);
-                                const float al = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - mn) : 0.f;
-                                m[nt][h] = mn;
-                                l[nt][h] *= al;
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    acc[nt][x][h] *= al;
-                                    acc[nt][x][2 + h] *= al;
-                                }
-                            }
-                    }
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) {
-                        uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float pr[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float mm = m[nt][e & 1];
-                                pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm : 0.f));
-                            }
-                            if constexpr (!FP8) {
-                                l[nt][0] += pr[0] + pr[2];
-                                l[nt][1] += pr[1] + pr[3];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const uint32_t h = pack2_bf16(pr[2 * e], pr[2 * e + 1]);
-                                    ph[nt][e] = transpose8(h);
-                                    pl[nt][e] = transpose8(pack2_bf16(pr[2 * e] - __uint_as_float(h << 16),
-                                                                      pr[2 * e + 1] - __uint_as_float(h & 0xffff0000u)));
-                                }
-                            } else {
-                                // l in units of 2^m: the scale's exponent taken back
-                                const float i0 = __uint_as_float((uint32_t)(127 - (int)ev[u][0]) << 23);
-                                const float i1 = __uint_as_float((uint32_t)(127 - (int)ev[u][1]) << 23);
-                                l[nt][0] += pr[0] * i0 + pr[2] * i1;
-                                l[nt][1] += pr[1] * i0 + pr[3] * i1;
-                                ph[nt][0] = transpose8(pack2_f16(pr[0], pr[1]));
-                                ph[nt][1] = transpose8(pack2_f16(pr[2], pr[3]));
-                            }
-                        }
-                        if constexpr (!FP8) {
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                const uint4 v0 = lds16(src + 4096 + (hh * 4 + 0) * 512), v1 = lds16(src + 4096 + (hh * 4 + 1) * 512);
-                                const uint4 v2 = lds16(src + 4096 + (hh * 4 + 2) * 512), v3 = lds16(src + 4096 + (hh * 4 + 3) * 512);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const uint32_t a0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5410);
-                                    const uint32_t a1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7632);
-                                    const uint32_t a2 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5410);
-                                    const uint32_t a3 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7632);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                                        mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-                                    }
-                                }
-                            }
-                        } else {
-                            const uint32_t vs = src + u * 4096 + 2048;
-                            const uint4 v0 = lds16(vs), v1 = lds16(vs + 512), v2 = lds16(vs + 1024), v3 = lds16(vs + 1536);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint32_t x0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5140);
-                                const uint32_t x1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7362);
-                                const uint32_t y0 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5140);
-                                const uint32_t y1 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7362);
-#pragma unroll
-                                for (int hf = 0; hf < 2; ++hf) {
-                                    const uint32_t xx = hf ? x1 : x0, yy = hf ? y1 : y0;
-                                    const uint32_t a0 = e4m3_f16(xx & 0xffffu), a1 = e4m3_f16(xx >> 16);
-                                    const uint32_t a2 = e4m3_f16(yy & 0xffffu), a3 = e4m3_f16(yy >> 16);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        mma_f16(acc[nt][2 * r + hf], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                                }
-                            }
-                        }
-                    }
-                }
-                if (++stage == kStepStages) stage = 0;
-            }
-            cp_wait<0>();
-
-            // ---- the four warps' states into one, in warp order
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o);
-                    if (j == 0) {
-                        s_m[warp * S::rows + nt * kGroup + 2 * i + h] = m[nt][h];
-                        s_l[warp * S::rows + nt * kGroup + 2 * i + h] = l[nt][h];
-                    }
-                }
-            __syncthreads();                                  // every warp's ring is drained, too
-            float* buf = reinterpret_cast<float*>(smem + S::ring) + warp * S::rows * kHD;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = nt * kGroup + 2 * i + h;
-                    float M = s_m[row];
-#pragma unroll
-                    for (int w = 1; w < kStepWarps; ++w) M = fmaxf(M, s_m[w * S::rows + row]);
-                    const float a = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - M) : 0.f;
+                const bool live = page >= 0;
+                const size_t row = live ? paged_row(c, page, head, key & slot_mask) : 0;
+                // rows outside [lo, hi) are not read: their slots may hold anything
+                auto on = [&](int r) { return live && key + r >= lo && key + r < hi; };
+                const uint8_t* kr = kp + row * kRowBytes;
+                const uint8_t* vr = vp + row * kRowBytes;
+                if constexpr (!FP8) {
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const int ch = FP8 ? 16 * j + 2 * x : (x >> 2) * 64 + 8 * j + 2 * (x & 3);
-                        *reinterpret_cast<float2*>(buf + row * kHD + ch) = make_float2(acc[nt][x][h] * a, acc[nt][x][2 + h] * a);
+                        const int r = j + (x >> 2) * 8;
+                        cp16(dst + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 3) * 4 + i) * 16 : 0), on(r));
                     }
-                }
-            if (tid < S::rows) {
-                float M = s_m[tid], l4 = 0.f;
 #pragma unroll
-                for (int w = 1; w < kStepWarps; ++w) M = fmaxf(M, s_m[w * S::rows + tid]);
-#pragma unroll
-                for (int w = 0; w < kStepWarps; ++w) {
-                    const float mw = s_m[w * S::rows + tid];
-                    l4 += s_l[w * S::rows + tid] * (mw > -INFINITY ? st_ex2(mw - M) : 0.f);
-                }
-                s_M[tid] = M;
-                s_L[tid] = l4;
-            }
-            __syncthreads();
-            const float* b0 = reinterpret_cast<const float*>(smem + S::ring) + tid;
-            const bool whole = t0 == 0 && t1 == grp.tiles;
-            const int rows = kGroup * grp.nrows;
-            const size_t out_row = (size_t)(row_b + grp.row0);
-            if (whole) {
-                for (int r = 0; r < rows; ++r) {
-                    float o = 0.f, v;
-#pragma unroll
-                    for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
-                    const int h = kGroup * head + (r & 7);
-                    o = step_finish(o, s_M[r], s_L[r], p.sinks[h], &v);
-                    const size_t tr = out_row + (r >> 3);
-                    p.out[(tr * nh + h) * kHD + tid] = __float2bfloat16_rn(o);
-                    if (tid == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
-                }
-                __syncthreads();
-                continue;
-            }
-            {
-                // slot 2 c: the CTA's first segment, 2 c + 1: a later one (its last)
-                float* dst = part + (2 * (size_t)cta + (t_first == t_begin ? 0 : 1)) * kPart;
-                if (tid < S::rows) {
-                    dst[tid] = s_M[tid];
-                    dst[16 + tid] = s_L[tid];
-                }
-                for (int r = 0; r < rows; ++r) {
-                    float o = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
-                    dst[32 + r * kHD + tid] = o;
-                }
-            }
-            // CTAs that hold a part of this segment: the owners of its first and last tile and all between
-            const long long cf = ((seg + 1) * G - 1) / W, cl = ((seg + grp.tiles) * G - 1) / W;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) *s_last = atomicAdd(arrive + (size_t)gi * ng + head, 1) == (int)(cl - cf);
-            __syncthreads();
-            if (*s_last) {
-                __threadfence();
-                const bool first_is_second = W * cf / G < seg;   // in its first CTA the segment is not the first one
-                for (int r = warp; r < rows; r += kStepWarps) {
-                    float M = -INFINITY;
-                    auto slot = [&](long long x) {
-                        return part + (2 * (size_t)x + (x == cf && first_is_second ? 1 : 0)) * kPart;
-                    };
-                    for (long long x = cf + lane; x <= cl; x += 32) M = fmaxf(M, __ldcg(slot(x) + r));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                    float Ls = 0.f;
-                    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (long long x = cf; x <= cl; ++x) {
-                        const float* s = slot(x);
-                        const float ms = __ldcg(s + r), ls = __ldcg(s + 16 + r);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 32 + r * kHD) + lane);
-                        const float a = ms > -INFINITY ? exp2f(ms - M) : 0.f;
-                        Ls += ls * a;
-                        o4.x += v.x * a;
-                        o4.y += v.y * a;
-                        o4.z += v.z * a;
-                        o4.w += v.w * a;
+                    for (int x = 0; x < 8; ++x) {
+                        const int r = 2 * i + (x & 1) + ((x >> 1) & 1) * 8;
+                        cp16(dst + 4096 + x * 512, vr + (on(r) ? r * kRowBytes + (x >> 2) * 128 + j * 16 : 0), on(r));
                     }
-                    const int h = kGroup * head + (r & 7);
-                    const size_t tr = out_row + (r >> 3);
-                    float v;
-                    const float sink = p.sinks[h];
-                    o4.x = step_finish(o4.x, M, Ls, sink, &v);
-                    o4.y = step_finish(o4.y, M, Ls, sink, &v);
-                    o4.z = step_finish(o4.z, M, Ls, sink, &v);
-                    o4.w = step_finish(o4.w, M, Ls, sink, &v);
-                    *reinterpret_cast<uint2*>(p.out + (tr * nh + h) * kHD + 4 * lane) =
-                        make_uint2(pack2_bf16(o4.x, o4.y), pack2_bf16(o4.z, o4.w));
-                    if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = j + (x >> 1) * 8;
+                        cp16(dst + u * 4096 + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 1) * 4 + i) * 16 : 0), on(r));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = 2 * i + (x & 1) + (x >> 1) * 8;
+                        cp16(dst + u * 4096 + 2048 + x * 512, vr + (on(r) ? r * kRowBytes + j * 16 : 0), on(r));
+                    }
+                    if (lane < 2) cp16(srow + stage * 64 + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + row, live);
                 }
             }
-            __syncthreads();
+            cp_commit();
+        };
+        int pg[kSub];
+        const int n_it = t1 - t0;
+        // the first stages on their way before the queries
+#pragma unroll
+        for (int s = 0; s < kStepStages - 1; ++s) {
+            if (s < n_it) {
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + s) * TL::tile + 16 * u);
+                issue(t0 + s, s, pg);
+            } else {
+                cp_commit();
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + kStepStages - 1) * TL::tile + 16 * u);
+
+        // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
+        if (warp < 2 * NT) {
+            const int nt = warp >> 1, sub = lane & 7, hh = 4 * (warp & 1) + (lane >> 3);
+            const bool have = nt < grp.nrows;
+            const int pos = p0 + (have ? nt : 0);
+            const __nv_bfloat16* src =
+                p.q + ((size_t)(row_b + grp.row0 + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
+            const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * sub);
+            const uint4 b = *reinterpret_cast<const uint4*>(src + 64 + 8 * sub);
+            float x0[8], x1[8], ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t aw = reg4(a, e >> 1), bw = reg4(b, e >> 1);
+                x0[e] = (e & 1) ? __uint_as_float(aw & 0xffff0000u) : __uint_as_float(aw << 16);
+                x1[e] = (e & 1) ? __uint_as_float(bw & 0xffff0000u) : __uint_as_float(bw << 16);
+                ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+            }
+            ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+            ss += __shfl_xor_sync(0xffffffffu, ss, 4);
+            const float rn = qscale / sqrtf(ss * (1.f / kHD) + p.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x0[e] *= rn * p.q_norm_w[8 * sub + e];
+                x1[e] *= rn * p.q_norm_w[64 + 8 * sub + e];
+            }
+            if (p.use_rope) {
+                const double* inv = reinterpret_cast<const double*>(p.ws + L.inv);
+                float c0, s0, c1, s1;
+                rope_cos_sin_exact(pos, inv[2 * lane], &c0, &s0);
+                rope_cos_sin_exact(pos, inv[2 * lane + 1], &c1, &s1);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int f = 8 * sub + e;
+                    const float cc = __shfl_sync(0xffffffffu, (e & 1) ? c1 : c0, f >> 1);
+                    const float sn = __shfl_sync(0xffffffffu, (e & 1) ? s1 : s0, f >> 1);
+                    const float y0 = x0[e] * cc - x1[e] * sn, y1 = x1[e] * cc + x0[e] * sn;
+                    x0[e] = y0;
+                    x1[e] = y1;
+                }
+            }
+            __half* qh = reinterpret_cast<__half*>(smem + S::q) + (nt * kGroup + hh) * kHD + 8 * sub;
+            __half* ql = qh + S::rows * kHD;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!have) x0[e] = x1[e] = 0.f;
+                const __half h0 = __float2half_rn(x0[e]), h1 = __float2half_rn(x1[e]);
+                qh[e] = h0;
+                qh[64 + e] = h1;
+                ql[e] = __float2half_rn(x0[e] - __half2float(h0));
+                ql[64 + e] = __float2half_rn(x1[e] - __half2float(h1));
+            }
+        }
+        __syncthreads();
+        // B fragments of q~ (head j, the lane's channels): [high, low][NT][16]
+        uint32_t qf[2][NT][16];
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    // 16-bit: chunk 4 x + i of 8 channels; 8-bit: the x % 2 half of chunk 4 (x / 2) + i of 16
+                    const int ch = FP8 ? ((x >> 1) * 4 + i) * 16 + (x & 1) * 8 : (x * 4 + i) * 8;
+                    const uint4 v = lds16(sb + S::q + ((pt * S::rows + nt * kGroup + j) * kHD + ch) * 2);
+                    qf[pt][nt][4 * x] = v.x;
+                    qf[pt][nt][4 * x + 1] = v.y;
+                    qf[pt][nt][4 * x + 2] = v.z;
+                    qf[pt][nt][4 * x + 3] = v.w;
+                }
+
+        // ---- the stream
+        float acc[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) acc[nt][x][0] = acc[nt][x][1] = acc[nt][x][2] = acc[nt][x][3] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+        int stage = 0;
+        for (int it = 0; it < n_it; ++it) {
+            // the stage after next, into the buffer read in the last iteration
+            if (it + kStepStages - 1 < n_it) {
+                int st2 = stage + kStepStages - 1;
+                if (st2 >= kStepStages) st2 -= kStepStages;
+                issue(t0 + it + kStepStages - 1, st2, pg);
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + it + kStepStages) * TL::tile + 16 * u);
+            } else {
+                cp_commit();
+            }
+            cp_wait<kStepStages - 1>();
+            if (FP8) __syncwarp();                        // the scales were fetched by other lanes
+            const uint32_t src = ring + stage * kStepStageBytes;
+            const int key0 = key_base + (t0 + it) * TL::tile;
+            if (key0 < hi && key0 + TL::block > lo) {
+                // scores: s[u][nt][0..3] = (key j, heads 2i, 2i + 1), (key j + 8, the same)
+                float s[kSub][NT][4];
+                float ev[kSub][2];
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    float sl[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[u][nt][e] = sl[nt][e] = 0.f;
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint4 a = lds16(src + x * 512), b = lds16(src + (4 + x) * 512);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_f16(s[u][nt], a.x, b.x, a.y, b.y, qf[0][nt][4 * x], qf[0][nt][4 * x + 1]);
+                                mma_f16(sl[nt], a.x, b.x, a.y, b.y, qf[1][nt][4 * x], qf[1][nt][4 * x + 1]);
+                                mma_f16(s[u][nt], a.z, b.z, a.w, b.w, qf[0][nt][4 * x + 2], qf[0][nt][4 * x + 3]);
+                                mma_f16(sl[nt], a.z, b.z, a.w, b.w, qf[1][nt][4 * x + 2], qf[1][nt][4 * x + 3]);
+                            }
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[u][nt][e] = (s[u][nt][e] + sl[nt][e]) * C;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint4 a = lds16(src + u * 4096 + x * 512), b = lds16(src + u * 4096 + (2 + x) * 512);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint32_t aw = reg4(a, r), bw = reg4(b, r);
+                                const uint32_t a0 = e4m3_f16(aw & 0xffffu), a2 = e4m3_f16(aw >> 16);
+                                const uint32_t a1 = e4m3_f16(bw & 0xffffu), a3 = e4m3_f16(bw >> 16);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    const int f = 8 * x + 2 * r;
+                                    mma_f16(s[u][nt], a0, a1, a2, a3, qf[0][nt][f], qf[0][nt][f + 1]);
+                                    mma_f16(sl[nt], a0, a1, a2, a3, qf[1][nt][f], qf[1][nt][f + 1]);
+                                }
+                            }
+                        }
+                        const uint8_t* ssc = smem + S::scales + (warp * kStepStages + stage) * 64 + u * 32;
+                        const float k0 = paged_scale(ssc[j]) * C, k1 = paged_scale(ssc[j + 8]) * C;
+                        ev[u][0] = (float)((int)ssc[16 + j] - 127);
+                        ev[u][1] = (float)((int)ssc[24 + j] - 127);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                s[u][nt][e] = fmaf(s[u][nt][e] + sl[nt][e], e < 2 ? k0 : k1, ev[u][e >> 1]);
+                    }
+                }
+                // masks: only where some row does not see the whole block
+                if (key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window)) {
+#pragma unroll
+                    for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int pos = p0 + nt, wl = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int k = key0 + 16 * u + j + (e >> 1) * 8;
+                                if (k > pos || k < wl) s[u][nt][e] = -INFINITY;
+                            }
+                        }
+                        // slots that hold no key of this call have any scale
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = key0 + 16 * u + j + 8 * e;
+                            if (k < lo || k >= hi) ev[u][e] = 0.f;
+                        }
+                    }
+                }
+                // raise the running max where a score passes it by 2^8
+                bool up = false;
+#pragma unroll
+                for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) up = up || s[u][nt][e] > m[nt][e & 1] + 8.f;
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float mx = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
+                            if (kSub == 2) mx = fmaxf(mx, fmaxf(s[kSub - 1][nt][h], s[kSub - 1][nt][2 + h]));
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            const float mn = fmaxf(m[nt][h], mx);
+                            const float al = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - mn) : 0.f;
+                            m[nt][h] = mn;
+                            l[nt][h] *= al;
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                acc[nt][x][h] *= al;
+                                acc[nt][x][2 + h] *= al;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+                    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float pr[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float mm = m[nt][e & 1];
+                            pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm : 0.f));
+                        }
+                        if constexpr (!FP8) {
+                            l[nt][0] += pr[0] + pr[2];
+                            l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t h = pack2_bf16(pr[2 * e], pr[2 * e + 1]);
+                                ph[nt][e] = transpose8(h);
+                                pl[nt][e] = transpose8(pack2_bf16(pr[2 * e] - __uint_as_float(h << 16),
+                                                                  pr[2 * e + 1] - __uint_as_float(h & 0xffff0000u)));
+                            }
+                        } else {
+                            // l in units of 2^m: the scale's exponent taken back
+                            const float i0 = __uint_as_float((uint32_t)(127 - (int)ev[u][0]) << 23);
+                            const float i1 = __uint_as_float((uint32_t)(127 - (int)ev[u][1]) << 23);
+                            l[nt][0] += pr[0] * i0 + pr[2] * i1;
+                            l[nt][1] += pr[1] * i0 + pr[3] * i1;
+                            ph[nt][0] = transpose8(pack2_f16(pr[0], pr[1]));
+                            ph[nt][1] = transpose8(pack2_f16(pr[2], pr[3]));
+                        }
+                    }
+                    if constexpr (!FP8) {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const uint4 v0 = lds16(src + 4096 + (hh * 4 + 0) * 512), v1 = lds16(src + 4096 + (hh * 4 + 1) * 512);
+                            const uint4 v2 = lds16(src + 4096 + (hh * 4 + 2) * 512), v3 = lds16(src + 4096 + (hh * 4 + 3) * 512);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint32_t a0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5410);
+                                const uint32_t a1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7632);
+                                const uint32_t a2 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5410);
+                                const uint32_t a3 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7632);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                                    mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                                }
+                            }
+                        }
+                    } else {
+                        const uint32_t vs = src + u * 4096 + 2048;
+                        const uint4 v0 = lds16(vs), v1 = lds16(vs + 512), v2 = lds16(vs + 1024), v3 = lds16(vs + 1536);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t x0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5140);
+                            const uint32_t x1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7362);
+                            const uint32_t y0 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5140);
+                            const uint32_t y1 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7362);
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t xx = hf ? x1 : x0, yy = hf ? y1 : y0;
+                                const uint32_t a0 = e4m3_f16(xx & 0xffffu), a1 = e4m3_f16(xx >> 16);
+                                const uint32_t a2 = e4m3_f16(yy & 0xffffu), a3 = e4m3_f16(yy >> 16);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma_f16(acc[nt][2 * r + hf], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                            }
+                        }
+                    }
+                }
+            }
+            if (++stage == kStepStages) stage = 0;
+        }
+        cp_wait<0>();
+
+        // ---- the four warps' states into one, in warp order
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o);
+                if (j == 0) {
+                    s_m[warp * S::rows + nt * kGroup + 2 * i + h] = m[nt][h];
+                    s_l[warp * S::rows + nt * kGroup + 2 * i + h] = l[nt][h];
+                }
+            }
+        __syncthreads();                                  // every warp's ring is drained, too
+        float* buf = reinterpret_cast<float*>(smem + S::ring) + warp * S::rows * kHD;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = nt * kGroup + 2 * i + h;
+                float M = s_m[row];
+#pragma unroll
+                for (int w = 1; w < kStepWarps; ++w) M = fmaxf(M, s_m[w * S::rows + row]);
+                const float a = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - M) : 0.f;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int ch = FP8 ? 16 * j + 2 * x : (x >> 2) * 64 + 8 * j + 2 * (x & 3);
+                    *reinterpret_cast<float2*>(buf + row * kHD + ch) = make_float2(acc[nt][x][h] * a, acc[nt][x][2 + h] * a);
+                }
+            }
+        if (tid < S::rows) {
+            float M = s_m[tid], l4 = 0.f;
+#pragma unroll
+            for (int w = 1; w < kStepWarps; ++w) M = fmaxf(M, s_m[w * S::rows + tid]);
+#pragma unroll
+            for (int w = 0; w < kStepWarps; ++w) {
+                const float mw = s_m[w * S::rows + tid];
+                l4 += s_l[w * S::rows + tid] * (mw > -INFINITY ? st_ex2(mw - M) : 0.f);
+            }
+            s_M[tid] = M;
+            s_L[tid] = l4;
+        }
+        __syncthreads();
+        const float* b0 = reinterpret_cast<const float*>(smem + S::ring) + tid;
+        const int rows = kGroup * grp.nrows;
+        const size_t out_row = (size_t)(row_b + grp.row0);
+        if (sg.whole) {
+            for (int r = 0; r < rows; ++r) {
+                float o = 0.f, v;
+#pragma unroll
+                for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
+                const int h = kGroup * head + (r & 7);
+                float sc;
+                paged_finish(s_M[r], s_L[r], p.sinks[h], &sc, &v);
+                o *= sc;
+                const size_t tr = out_row + (r >> 3);
+                p.out[(tr * nh + h) * kHD + tid] = __float2bfloat16_rn(o);
+                if (tid == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
+            }
+            __syncthreads();
+            continue;
+        }
+        {
+            // slot 2 c: the CTA's first segment, 2 c + 1: a later one (its last)
+            float* dst = part + (2 * (size_t)blockIdx.x + (sg.first ? 0 : 1)) * kStepPart;
+            if (tid < S::rows) {
+                dst[tid] = s_M[tid];
+                dst[16 + tid] = s_L[tid];
+            }
+            for (int r = 0; r < rows; ++r) {
+                float o = 0.f;
+#pragma unroll
+                for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
+                dst[32 + r * kHD + tid] = o;
+            }
+        }
+        // CTAs that hold a part of this segment: the owners of its first and last tile and all between
+        const long long cf = paged_owner(share.W, share.G, sg.seg), cl = paged_owner(share.W, share.G, sg.seg + grp.tiles - 1);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) *s_last = atomicAdd(arrive + (size_t)sg.gi * ng + head, 1) == (int)(cl - cf);
+        __syncthreads();
+        if (*s_last) {
+            __threadfence();
+            for (int r = warp; r < rows; r += kStepWarps) {
+                float M = -INFINITY;
+                auto slot = [&](long long x) { return part + paged_slot(share.W, share.G, sg.seg, x) * kStepPart; };
+                for (long long x = cf + lane; x <= cl; x += 32) M = fmaxf(M, __ldcg(slot(x) + r));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                float Ls = 0.f;
+                float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                for (long long x = cf; x <= cl; ++x) {
+                    const float* s = slot(x);
+                    const float ms = __ldcg(s + r), ls = __ldcg(s + 16 + r);
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 32 + r * kHD) + lane);
+                    const float a = ms > -INFINITY ? exp2f(ms - M) : 0.f;
+                    Ls += ls * a;
+                    o4.x += v.x * a;
+                    o4.y += v.y * a;
+                    o4.z += v.z * a;
+                    o4.w += v.w * a;
+                }
+                const int h = kGroup * head + (r & 7);
+                const size_t tr = out_row + (r >> 3);
+                float sc, v;
+                paged_finish(M, Ls, p.sinks[h], &sc, &v);
+                *reinterpret_cast<uint2*>(p.out + (tr * nh + h) * kHD + 4 * lane) =
+                    make_uint2(pack2_bf16(o4.x * sc, o4.y * sc), pack2_bf16(o4.z * sc, o4.w * sc));
+                if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
+            }
+        }
+        __syncthreads();
     }
 }
 
 // ============================================================================ host
 namespace {
-
-int step_ctas(int sms) { return sms * kStepCtasPerSm; }
 
 template <int NT, bool FP8>
 cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
@@ -772,7 +785,7 @@ cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
         set[dev & 63] = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas);
+    cfg.gridDim = dim3(p.step_ctas);
     cfg.blockDim = dim3(kStepThreads);
     cfg.dynamicSmemBytes = StepSmem<NT>::total;
     cfg.stream = s;
@@ -784,30 +797,36 @@ cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, paged_step_kernel<NT, FP8>, p);
 }
 
-}  // namespace
-
-// The workspace does not depend on the device: partials for the step
-// kernel's CTAs on a full B200 (148 SMs).
+// The workspace does not depend on the device: room for a full B200's CTAs.
 constexpr int kPagedMaxSms = 148;
 
+// Calls whose sequences all have at most this many new tokens run the step
+// kernel alone.
+constexpr int kStepMaxNew = 8;
+
+}  // namespace
+
 size_t paged_attn_workspace(int B, int T, int max_new, int ng) {
-    (void)B;
-    (void)max_new;
-    return paged_ws(T, ng, step_ctas(kPagedMaxSms)).total;
+    return paged_ws(B, T, ng, kPagedMaxSms * kStepCtasPerSm, max_new > kStepMaxNew ? kPagedMaxSms : 0).total;
 }
 
 flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, cudaStream_t s) {
     PagedAttnParams p = in;
-    p.ctas = step_ctas(sms < kPagedMaxSms ? sms : kPagedMaxSms);
+    if (sms > kPagedMaxSms) sms = kPagedMaxSms;
+    p.step_ctas = sms * kStepCtasPerSm;
+    p.chunk_ctas = p.max_new > kStepMaxNew ? sms : 0;
     const bool fp8 = p.k_scales != nullptr;
     const int nt = p.max_new > 1 ? 2 : 1;
-    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, nt, fp8 ? StepTile<true>::tile : StepTile<false>::tile);
+    // with the chunk kernel in the call, it takes every sequence
+    const PagedListSpec step = {1, p.chunk_ctas ? 0 : 0x7fffffff, nt, fp8 ? StepTile<true>::tile : StepTile<false>::tile, 16};
+    const PagedListSpec chunk = {1, 0x7fffffff, kChunkTok, kKeyChunk, 1 << c.ps_log2};
+    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, step, chunk);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !p.chunk_ctas)
         e = nt == 1 ? (fp8 ? launch_step<1, true>(p, s) : launch_step<1, false>(p, s))
                     : (fp8 ? launch_step<2, true>(p, s) : launch_step<2, false>(p, s));
     if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
-    return FLINT_OK;
+    return p.chunk_ctas ? launch_paged_chunk(p, s) : FLINT_OK;
 }
 
 }  // namespace flint

@@ -15,6 +15,8 @@ Tolerances, from the roundings that the kernels make:
   the running sums).  P is kept to 2^-16 (two BF16 parts; 8-bit values: 2^-11
   once, in FP16), its sums and the exponential to 2^-16: 2 dz + 2^-15 of A
   (8-bit values: + 2^-11).  LSE: dz and an FP32 last place or two of itself.
+  The chunk kernel (a sequence of the call has over 8 new tokens) rounds q~ to
+  FP16 and P to BF16: dz = 2^-11 spread + 2e-5 and 2^-8 + 2 dz of A.
 """
 import numpy as np
 import pytest
@@ -117,7 +119,7 @@ LENS = {
     "some_none": ([5, 40, 0, 129, 64], [1, 0, 0, 1, 0]),
     "pairs": ([0, 14, 31, 100, 250, 511], [2, 2, 2, 1, 2, 2]),
     "few": ([0, 3, 60, 127, 300], [3, 5, 1, 8, 7]),
-    "rows": ([0, 100, 37, 5], [40, 17, 1, 33]),
+    "rows": ([0, 100, 37, 5, 511], [40, 17, 1, 33, 9]),
 }
 FORMS = [(16, False, 4), (32, True, 4), (64, False, 2), (128, True, 1), (64, True, 2), (128, False, 1)]
 
@@ -135,7 +137,7 @@ def test_append_and_attend(fa, lens, ps, fp8, g, window, rope):
     lse = torch.full((8 * g, c.T), 7.0, device="cuda")
     st, out, lse = attend(fa, c, t, out=out, lse=lse)
     assert st == 0
-    check_attend(c, t, out, lse)
+    check_attend(c, t, out, lse, chunk=c.new.max() > 8)
     assert (out[c.rows:] == 7).all() and (lse[:, c.rows:] == 7).all()
 
 
@@ -171,6 +173,21 @@ def test_long_axis_is_split_and_repeatable(fa, fp8):
     for _ in range(3):
         _, o2, l2 = attend(fa, c, t)
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("ps,fp8", [(16, False), (128, False), (64, True)])
+@pytest.mark.parametrize("ctx,new,window", [([2500], [70], 0), ([900, 0, 130, 4000, 64], [33, 129, 16, 1, 100], 0),
+                                            ([700, 5000, 0], [300, 40, 17], 257)])
+def test_chunks(fa, ps, fp8, ctx, new, window):
+    c = Case(ctx, new, ps=ps, fp8=fp8, window=window, rope=window > 0, seed=8, extra=2)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, out, lse = attend(fa, c, t)
+    assert st == 0
+    check_attend(c, t, out, lse, chunk=True)
+    for _ in range(2):
+        _, o2, l2 = attend(fa, c, t)
+        assert torch.equal(out[:c.rows], o2[:c.rows]) and torch.equal(lse[:, :c.rows], l2[:, :c.rows])
 
 
 @pytest.mark.parametrize("fp8", [False, True])
