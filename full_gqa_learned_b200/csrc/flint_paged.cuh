@@ -102,7 +102,11 @@ struct PagedAttnParams {
 // A row group: consecutive new tokens of one sequence that a kernel takes
 // together (at most `nt` of its list).  Its tiles are runs of positions from
 // the aligned start of what its rows see.
-struct PagedGroup { int b, row0, nrows, tiles; };
+struct PagedGroup {
+    int b, nrows, tiles;
+    int p0;                      // position of its first row
+    int row;                     // packed row of its first row
+};
 
 // The work of one kernel: the tiles of all (group, KV head) pairs in a row,
 // group by group, head by head.  The plan kernel writes the groups and the
@@ -170,55 +174,72 @@ __device__ __forceinline__ void paged_finish(float M, float L, float sink, float
     *lse = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 }
 
-// One (group, head) pair's part of a CTA's share.
+// A CTA's share, walked pair by pair.  The pair's place among all W tiles is
+// needed only where it is held in part (paged_seg_begin).
 struct PagedShare {
     const PagedGroup* groups;
-    const long long* prefix;
-    long long W, G;              // tiles of all pairs, CTAs that share them
-    long long t, t_begin, t_end; // the CTA's share; t: next tile
-    int gi, head, ng;
+    int ng, gi, head, off;       // the next pair; off: tile of it that the share enters at
+    int left;                    // tiles left in the share
 };
 struct PagedSeg {
     PagedGroup g;
-    long long seg;               // the pair's first tile, of all W
-    int gi, head, t0, t1;        // this CTA's tiles [t0, t1) of the pair
-    bool whole, first;           // all of it; the CTA's first pair
+    int gi, head, t0, t1;        // tiles [t0, t1) of pair (gi, head)
+    bool whole;                  // all of it
+    bool first;                  // the share's first pair
 };
 __device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedList& l, const PagedGroup* groups,
                                                   const long long* prefix, int ng, int cta, int ctas) {
+    const long long W = l.tiles * ng;
+    const long long G = W < (long long)ctas ? W : (long long)ctas;
+    if (cta >= G) return false;
+    const long long t = W * cta / G;
     s.groups = groups;
-    s.prefix = prefix;
     s.ng = ng;
-    s.W = l.tiles * ng;
-    s.G = s.W < (long long)ctas ? s.W : (long long)ctas;
-    if (cta >= s.G) return false;
-    s.t = s.t_begin = s.W * cta / s.G;
-    s.t_end = s.W * (cta + 1) / s.G;
-    s.gi = warp_last_leq(prefix, l.n, s.t / ng);
-    s.head = (int)((s.t - prefix[s.gi] * ng) / groups[s.gi].tiles);
+    s.left = (int)(W * (cta + 1) / G - t);
+    s.gi = warp_last_leq(prefix, l.n, t / ng);
+    const long long in = t - prefix[s.gi] * ng;
+    const int tiles = groups[s.gi].tiles;
+    s.head = (int)(in / tiles);
+    s.off = (int)(in - (long long)s.head * tiles);
     return true;
 }
-__device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g) {
-    if (s.t >= s.t_end) return false;
-    if (s.head == s.ng) { s.head = 0; ++s.gi; }
+__device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g, bool first) {
+    if (s.left <= 0) return false;
     g.g = s.groups[s.gi];
     g.gi = s.gi;
     g.head = s.head;
-    g.seg = s.prefix[s.gi] * s.ng + (long long)s.head * g.g.tiles;
-    g.t0 = (int)(s.t - g.seg);
-    g.t1 = (int)(g.g.tiles < s.t_end - g.seg ? (long long)g.g.tiles : s.t_end - g.seg);
+    g.t0 = s.off;
+    g.t1 = min(g.g.tiles, s.off + s.left);
     g.whole = g.t0 == 0 && g.t1 == g.g.tiles;
-    g.first = s.t == s.t_begin;
-    s.t += g.t1 - g.t0;
-    ++s.head;
+    g.first = first;
+    s.left -= g.t1 - g.t0;
+    s.off = 0;
+    if (++s.head == s.ng) { s.head = 0; ++s.gi; }
     return true;
+}
+// The first of all W tiles that is pair (gi, head)'s.
+__device__ __forceinline__ long long paged_seg_begin(const long long* prefix, const PagedSeg& g, int ng) {
+    return prefix[g.gi] * ng + (long long)g.head * g.g.tiles;
 }
 // The CTA that owns tile x.
 __device__ __forceinline__ long long paged_owner(long long W, long long G, long long x) { return ((x + 1) * G - 1) / W; }
-// The partial that CTA `cta` leaves of the pair that starts at tile seg: 2 c
-// where it is the CTA's first pair, else 2 c + 1.
-__device__ __forceinline__ size_t paged_slot(long long W, long long G, long long seg, long long cta) {
-    return 2 * (size_t)cta + (W * cta / G < seg ? 1 : 0);
+// The CTAs cf .. cl that hold parts of a pair, and where they left them: a
+// CTA's first pair in slot 2 c, a later one (its last) in 2 c + 1.  Every CTA
+// but cf begins inside the pair.
+struct PagedParts {
+    int cf, cl;
+    bool second;                 // in cf's share it is not the first pair
+    __device__ __forceinline__ size_t slot(int x) const { return 2 * (size_t)x + (x == cf && second ? 1 : 0); }
+};
+__device__ __forceinline__ PagedParts paged_parts(const PagedList& l, const long long* prefix, const PagedSeg& g, int ng,
+                                                  int ctas) {
+    const long long W = l.tiles * ng, G = W < (long long)ctas ? W : (long long)ctas;
+    const long long seg = paged_seg_begin(prefix, g, ng);
+    PagedParts r;
+    r.cf = (int)paged_owner(W, G, seg);
+    r.cl = (int)paged_owner(W, G, seg + g.g.tiles - 1);
+    r.second = W * r.cf / G < seg;
+    return r;
 }
 
 }  // namespace flint

@@ -76,10 +76,10 @@ struct PcMisc {
 // the control warps give theirs to the softmax warpgroups.
 template <bool FP8> struct PcShape {
     static constexpr int threads = FP8 ? 512 : 384;
-    static constexpr uint32_t control = FP8 ? 56 : 80, softmax = FP8 ? 184 : 208, convert = 88;
+    static constexpr uint32_t control = FP8 ? 40 : 80, softmax = FP8 ? 184 : 208, convert = 104;
 };
 static_assert(128 * 80 + 256 * 208 <= 384 * 168, "register split");
-static_assert(128 * 56 + 128 * 88 + 256 * 184 <= 512 * 128, "register split, 8-bit pages");
+static_assert(128 * 40 + 128 * 104 + 256 * 184 <= 512 * 128, "register split, 8-bit pages");
 
 __device__ __forceinline__ float pc_ex2(float x) {
     float y;
@@ -135,11 +135,11 @@ struct PcGroup {
 };
 __device__ __forceinline__ PcGroup pc_group(const PagedAttnParams& p, const PagedGroup& g) {
     PcGroup r;
-    r.p0 = p.c.len[g.b] + g.row0;
+    r.p0 = g.p0;
     r.hi = r.p0 + g.nrows;
     r.lo = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
     r.kb = r.lo & ~((1 << p.c.ps_log2) - 1);
-    r.row = p.c.cu[g.b] + g.row0;
+    r.row = g.row;
     return r;
 }
 // Columns of the chunk that starts at ks: up to the group's last position,
@@ -216,6 +216,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const uint32_t tmem = misc->tmem_base;
     PagedShare share;
     PagedSeg sg;
+    bool first = true;
     const bool work = paged_share_begin(share, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.cgroups),
                                         reinterpret_cast<const long long*>(p.ws + L.cprefix), ng, blockIdx.x, gridDim.x);
 
@@ -227,7 +228,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ============================================================ producer (the whole warp)
         uint32_t qph[2] = {0u, 0u}, st = 0, ph = 0, narm_q[2] = {0u, 0u}, narm = 0;
         bool ok = true;
-        while (ok && paged_share_next(share, sg)) {
+        for (; ok && paged_share_next(share, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
             const int ntile = sg.g.nrows > kTokPerTile ? 2 : 1;
             for (int t = 0; t < ntile && ok; ++t) {
@@ -330,7 +331,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // lane 0 waits and issues, the others follow its outcome
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qrph[2] = {0u, 0u}, pph[2] = {0u, 0u};
         bool ok = true;
-        while (ok && paged_share_next(share, sg)) {
+        for (; ok && paged_share_next(share, sg, first); first = false) {
             if (lane == 0) {
                 const PcGroup gr = pc_group(p, sg.g);
                 const int ntile = sg.g.nrows > kTokPerTile ? 2 : 1, n = sg.t1 - sg.t0;
@@ -395,7 +396,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ============================================================ V rows without a position
         uint32_t st = 0, ph = 0;
         bool ok = true;
-        while (ok && paged_share_next(share, sg)) {
+        for (; ok && paged_share_next(share, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
             for (int ch = sg.t0; ch < sg.t1; ++ch) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_FULL + st), ph, abort_flag, status));
@@ -421,58 +422,64 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     } else if (FP8 && warp >= 12) {
         regs_dec<PcShape<FP8>::convert>();
         // ============================================================ 8-bit pages: codes and scales -> FP16 K, BF16 V
-        // Warp w takes rows 32 w .. 32 w + 31 of each chunk, four at a time,
-        // eight lanes a row of 128 codes; rows without a position become zeros.
-        const int w = warp - 12, sub = lane & 7, rl = lane >> 3;
+        // Warp w takes rows 32 w .. 32 w + 31 of each chunk, four at a time:
+        // lane (a, b, s) = bits (4-3, 2, 1-0) holds codes 16 sub .. + 15, sub =
+        // 4 (a / 2) + s, of row 2 (a % 2) + b, so that the eight lanes of a
+        // store phase, rows of both parities, meet no bank twice.  K's and V's
+        // codes are fetched one chunk ahead of their conversion.  Rows without
+        // a position become zeros.
+        const int w = warp - 12, sub = 4 * (lane >> 4) + (lane & 3), rl = 2 * ((lane >> 3) & 1) + ((lane >> 2) & 1);
         const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
         const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
         uint32_t st = 0, ph = 0;
         bool ok = true;
-        while (ok && paged_share_next(share, sg)) {
+        for (; ok && paged_share_next(share, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
             const int* table = c.table + (size_t)sg.g.b * c.max_pages;
-            for (int ch = sg.t0; ch < sg.t1; ++ch) {
-                const int ks = gr.kb + kKeyChunk * ch + 32 * w;
-                // pool rows of the warp's 32 positions: lane l holds position
-                // ks + l; -1 where there is none
-                long long row = -1;
-                {
-                    const int pos = ks + lane;
-                    if (pos >= gr.lo && pos < gr.hi) {
-                        const int page = __ldg(table + (pos >> c.ps_log2));
-                        if (page >= 0 && page < c.num_pages)
-                            row = (long long)paged_row(c, page, sg.head, pos & ((1 << c.ps_log2) - 1));
-                        else
-                            atomicCAS(status, 0, kStatusInvalid);
-                    }
+            // Pages of the warp's 32 positions of chunk ch, lane l's position
+            // ks + l: -1 none, -2 no position.
+            auto page_of = [&](int ch) -> int {
+                const int pos = gr.kb + kKeyChunk * ch + 32 * w + lane;
+                return ch < sg.t1 && pos >= gr.lo && pos < gr.hi ? __ldg(table + (pos >> c.ps_log2)) : -2;
+            };
+            // Row of the pools, or -1.
+            auto row_of = [&](int page, int ch) -> long long {
+                if (page == -2) return -1;
+                if (page < 0 || page >= c.num_pages) {
+                    atomicCAS(status, 0, kStatusInvalid);
+                    return -1;
                 }
-                auto load = [&](const uint8_t* pages, uint4* x) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const long long r = __shfl_sync(0xffffffffu, row, 4 * i + rl);
-                        x[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(pages + r * kHD) + sub) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-                };
-                const uint32_t sk = row >= 0 ? __ldg(p.k_scales + row) : 127u;
-                const uint32_t sv = row >= 0 ? __ldg(p.v_scales + row) : 127u;
-                uint4 x[8];
-                load(kp, x);
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_K_EMPTY + st), ph ^ 1, abort_flag, status));
-                if (!ok) break;
-                // lane's channels 16 sub .. + 15: chunks 2 (sub % 4), + 1 of
-                // half sub / 4; the halves' lanes write them in opposite
-                // order, so a row's eight lanes meet no bank twice
-                auto place = [&](uint32_t tile, int r, uint4 a, uint4 b) {
-                    uint8_t* d = smem + tile + (sub >> 2) * kPcHalf + r * 128;
-                    const int c0 = 2 * (sub & 3), o = sub >> 2;
-                    *reinterpret_cast<uint4*>(d + (((c0 + o) ^ (r & 7)) << 4)) = o ? b : a;
-                    *reinterpret_cast<uint4*>(d + (((c0 + 1 - o) ^ (r & 7)) << 4)) = o ? a : b;
-                };
+                const int pos = gr.kb + kKeyChunk * ch + 32 * w + lane;
+                return (long long)paged_row(c, page, sg.head, pos & ((1 << c.ps_log2) - 1));
+            };
+            auto load = [&](const uint8_t* pages, long long row, uint4* x) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float s = paged_scale(__shfl_sync(0xffffffffu, sk, 4 * i + rl));
-                    const __half2 s2 = __float2half2_rn(s);
-                    const uint32_t cw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    const long long r = __shfl_sync(0xffffffffu, row, 4 * i + rl);
+                    x[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(pages + r * kHD) + sub) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto place = [&](uint32_t tile, int r, const uint32_t* h) {
+                uint8_t* d = smem + tile + (sub >> 2) * kPcHalf + r * 128;
+                const int c0 = 2 * (sub & 3);
+                *reinterpret_cast<uint4*>(d + ((c0 ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(d + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            };
+            long long row = row_of(page_of(sg.t0), sg.t0);
+            uint4 xk[8], xv[8];
+            load(kp, row, xk);
+            load(vp, row, xv);
+            uint32_t sk = row >= 0 ? __ldg(p.k_scales + row) : 127u, sv = row >= 0 ? __ldg(p.v_scales + row) : 127u;
+            int pg = page_of(sg.t0 + 1);
+            for (int ch = sg.t0; ch < sg.t1; ++ch) {
+                const long long next = row_of(pg, ch + 1);
+                pg = page_of(ch + 2);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_K_EMPTY + st), ph ^ 1, abort_flag, status));
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const __half2 s2 = __float2half2_rn(paged_scale(__shfl_sync(0xffffffffu, sk, 4 * i + rl)));
+                    const uint32_t cw[4] = {xk[i].x, xk[i].y, xk[i].z, xk[i].w};
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -481,18 +488,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), s2);
                         h[e] = *reinterpret_cast<const uint32_t*>(&y);
                     }
-                    place(kPcK + st * kPcTile, 32 * w + 4 * i + rl, make_uint4(h[0], h[1], h[2], h[3]), make_uint4(h[4], h[5], h[6], h[7]));
+                    place(kPcK + st * kPcTile, 32 * w + 4 * i + rl, h);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(PC_K_FULL + st));
-                load(vp, x);
+                load(kp, next, xk);
+                sk = next >= 0 ? __ldg(p.k_scales + next) : 127u;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_EMPTY + st), ph ^ 1, abort_flag, status));
                 if (!ok) break;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float s = paged_scale(__shfl_sync(0xffffffffu, sv, 4 * i + rl));
-                    const uint32_t cw[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    const uint32_t cw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -501,11 +509,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
                         h[e] = pc_pack_bf16(f.x * s, f.y * s);
                     }
-                    place(kPcV + st * kPcTile, 32 * w + 4 * i + rl, make_uint4(h[0], h[1], h[2], h[3]), make_uint4(h[4], h[5], h[6], h[7]));
+                    place(kPcV + st * kPcTile, 32 * w + 4 * i + rl, h);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(PC_V_FULL + st));
+                load(vp, next, xv);
+                sv = next >= 0 ? __ldg(p.v_scales + next) : 127u;
                 st ^= 1; if (st == 0) ph ^= 1;
             }
         }
@@ -524,8 +534,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t stg_s = sbase + kPcStage + (warp - 4) * kPcStageBytes;
         // The next pair this tile takes part in.
         auto fetch = [&]() -> bool {
-            while (paged_share_next(share, sg))
+            while (paged_share_next(share, sg, first)) {
+                first = false;
                 if (t == 0 || sg.g.nrows > kTokPerTile) return true;
+            }
             return false;
         };
         // Query prologue: thread r normalises row r of the tile in place
@@ -624,7 +636,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             float m = -INFINITY, l = 0.f;                            // the sink joins at the end
             bool alive = true;
             for (int ch = cur.t0; ch < cur.t1; ++ch) {
-                const bool first = ch == cur.t0;
+                const bool first_ch = ch == cur.t0;
                 const int ks = gr.kb + kKeyChunk * ch;
                 const int nc = pc_cols(ks, gr.hi);
                 const int nblk = (nc + 31) >> 5;
@@ -632,7 +644,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 s_ph ^= 1;
                 tc_fence_after();
                 const bool boundary = ks + kKeyChunk - 1 > pos0 || (p.window > 0 && ks < pos0 + kTokPerTile - p.window);
-                const bool fastp = !boundary && !first && __all_sync(0xffffffffu, m > -INFINITY && m < INFINITY);
+                const bool fastp = !boundary && !first_ch && __all_sync(0xffffffffu, m > -INFINITY && m < INFINITY);
                 uint32_t sv[128];
                 tmem_ld32(t_s, sv);
                 if (nblk > 1) tmem_ld32(t_s + 32u, sv + 32);
@@ -682,14 +694,14 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // Whether any row of the warp did.
                 auto raise_to = [&](float mx) -> bool {
                     const float m_new = fmaxf(m, mx * C);
-                    const bool raise = first ? (m_new > m) : (m_new > m + 8.f);
+                    const bool raise = first_ch ? (m_new > m) : (m_new > m + 8.f);
                     float alpha = 1.f;
                     if (raise) {
                         alpha = pc_ex2(m - m_new);
                         l *= alpha;
                     }
                     const bool any = __any_sync(0xffffffffu, raise);
-                    if (!first && any) {
+                    if (!first_ch && any) {
 #pragma unroll 1
                         for (int b = 0; b < 8; ++b) {
                             uint32_t v[16];
@@ -703,31 +715,48 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (raise) m = m_new;
                     return any;
                 };
-                // P = 2^(s C - m) -> BF16 over S, blocks b0 .. b1 - 1; the row sum
-                auto exp_part = [&](const int b0, const int b1) -> float {
-                    const float negm = m == -INFINITY ? 0.f : -m;
-                    const uint64_t C2 = f2(C, C), negm2 = f2(negm, negm);
-                    uint64_t lp[4] = {0ull, 0ull, 0ull, 0ull};
+                // P = 2^(s C - m) -> BF16 over S; the row sum.  Blocks b0 ..
+                // b1 - 1 of an unmasked chunk, free of branches:
+                auto exp_block = [&](const int b, uint64_t C2, uint64_t negm2, uint64_t* lp) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int b = b0; b < b1; ++b) {
-                        uint32_t pk[16];
-                        if (emptym & (1u << b)) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) pk[j] = 0u;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float2 x = f2_get(f2_fma(f2(__uint_as_float(sv[32 * b + 2 * j]),
-                                                                  __uint_as_float(sv[32 * b + 2 * j + 1])), C2, negm2));
-                                const float e0 = pc_ex2(x.x), e1 = pc_ex2(x.y);
-                                lp[j & 3] = f2_add(lp[j & 3], f2(e0, e1));
-                                pk[j] = pc_pack_bf16(e0, e1);
-                            }
-                        }
-                        if (b < nblk) tmem_st16(t_s + 16u * b, pk);
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 x = f2_get(f2_fma(f2(__uint_as_float(sv[32 * b + 2 * j]),
+                                                          __uint_as_float(sv[32 * b + 2 * j + 1])), C2, negm2));
+                        const float e0 = pc_ex2(x.x), e1 = pc_ex2(x.y);
+                        lp[j & 3] = f2_add(lp[j & 3], f2(e0, e1));
+                        pk[j] = pc_pack_bf16(e0, e1);
                     }
+                    tmem_st16(t_s + 16u * b, pk);
+                };
+                auto exp_sum = [&](const uint64_t* lp) -> float {
                     const float2 ls = f2_get(f2_add(f2_add(lp[0], lp[1]), f2_add(lp[2], lp[3])));
                     return ls.x + ls.y;
+                };
+                auto exp_part = [&](const int b0, const int b1) -> float {
+                    uint64_t lp[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int b = b0; b < b1; ++b) exp_block(b, f2(C, C), f2(-m, -m), lp);
+                    return exp_sum(lp);
+                };
+                // and with masks (masked columns are -inf already), empty
+                // blocks as zeros
+                auto exp_masked = [&]() -> float {
+                    const float negm = m == -INFINITY ? 0.f : -m;
+                    uint64_t lp[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (b >= nblk) continue;
+                        if (emptym & (1u << b)) {
+                            uint32_t z[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) z[j] = 0u;
+                            tmem_st16(t_s + 16u * b, z);
+                        } else {
+                            exp_block(b, f2(C, C), f2(negm, negm), lp);
+                        }
+                    }
+                    return exp_sum(lp);
                 };
                 float lsum = 0.f;
                 if (fastp) {
@@ -746,7 +775,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 } else {
                     raise_to(row_max());
-                    lsum = exp_part(0, 4);
+                    lsum = exp_masked();
                 }
                 l += lsum;
                 tmem_wait_st();
@@ -856,23 +885,24 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnParam
     const float* part = reinterpret_cast<const float*>(p.ws + L.cpart);
     griddep_wait();
     PagedShare s;
-    if (!paged_share_begin(s, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.cgroups),
-                           reinterpret_cast<const long long*>(p.ws + L.cprefix), ng, blockIdx.x + 1, p.chunk_ctas))
+    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.cprefix);
+    if (!paged_share_begin(s, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.cgroups), prefix, ng,
+                           blockIdx.x + 1, p.chunk_ctas))
         return;
     PagedSeg sg;
-    if (!paged_share_next(s, sg) || sg.t0 == 0) return;       // the share begins with a pair
-    const long long cf = paged_owner(s.W, s.G, sg.seg), cl = paged_owner(s.W, s.G, sg.seg + sg.g.tiles - 1);
-    if (cf != (long long)blockIdx.x) return;                  // an earlier block folds this pair
+    if (!paged_share_next(s, sg, true) || sg.t0 == 0) return;   // the share begins with a pair
+    const PagedParts pp = paged_parts(hdr->chunk, prefix, sg, ng, p.chunk_ctas);
+    if (pp.cf != (int)blockIdx.x) return;                       // an earlier block folds this pair
     const int row = 32 * blockIdx.y + lane, tok = row >> 3;
     if (4 * (int)blockIdx.y >= sg.g.nrows) return;
     float M = -INFINITY;
-    for (long long x = cf; x <= cl; ++x) M = fmaxf(M, part[paged_slot(s.W, s.G, sg.seg, x) * kChunkPart + row]);
+    for (int x = pp.cf; x <= pp.cl; ++x) M = fmaxf(M, part[pp.slot(x) * kChunkPart + row]);
     float l = 0.f;
     float4 o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long x = cf; x <= cl; ++x) {
-        const float* b = part + paged_slot(s.W, s.G, sg.seg, x) * kChunkPart;
+    for (int x = pp.cf; x <= pp.cl; ++x) {
+        const float* b = part + pp.slot(x) * kChunkPart;
         const float mx = b[row], lx = b[256 + row];
         const float a = mx > -INFINITY ? exp2f(mx - M) : 0.f;
         const float4* o4 = reinterpret_cast<const float4*>(b + 512) + (size_t)(8 * warp) * 256 + row;
@@ -890,7 +920,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnParam
     const int h = kGroup * sg.head + (row & 7);
     float scale, lse;
     paged_finish(M, l, p.sinks[h], &scale, &lse);
-    const size_t t = (size_t)(c.cu[sg.g.b] + sg.g.row0 + tok);
+    const size_t t = (size_t)(sg.g.row + tok);
     uint4* dst = reinterpret_cast<uint4*>(p.out + (t * nh + h) * kHD + 32 * warp);
 #pragma unroll
     for (int j = 0; j < 4; ++j)

@@ -133,7 +133,7 @@ __device__ void plan_list(const PagedAttnParams& p, const PagedListSpec& q, Page
     long long tiles = 0;
     for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
         const int g = g0 + tid;
-        PagedGroup r = {0, 0, 0, 0};
+        PagedGroup r = {};
         if (g < n_groups) {
             int lo = 0, hi = n_off - 1;                       // last entry with off <= g
             while (lo < hi) {
@@ -147,11 +147,12 @@ __device__ void plan_list(const PagedAttnParams& p, const PagedListSpec& q, Page
                 const int k = n >= q.n_min && n <= q.n_max ? (n + q.nt - 1) / q.nt : 0;
                 if (g < at + k || b == c.B - 1) {
                     r.b = b;
-                    r.row0 = (g - at) * q.nt;
-                    r.nrows = min(q.nt, n - r.row0);
-                    const int p0 = c.len[b] + r.row0;
-                    const int first = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-                    r.tiles = (p0 + r.nrows - (first & ~(q.align - 1)) + q.tile - 1) / q.tile;
+                    const int row0 = (g - at) * q.nt;
+                    r.nrows = min(q.nt, n - row0);
+                    r.p0 = c.len[b] + row0;
+                    r.row = c.cu[b] + row0;
+                    const int first = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
+                    r.tiles = (r.p0 + r.nrows - (first & ~(q.align - 1)) + q.tile - 1) / q.tile;
                     break;
                 }
                 at += k;
@@ -245,10 +246,10 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// two E4M3 codes -> two FP16 values (exact)
+// the two E4M3 codes in the low half of a word -> two FP16 values (exact)
 __device__ __forceinline__ uint32_t e4m3_f16(uint32_t codes) {
     uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(codes));
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
     return r;
 }
 __device__ __forceinline__ uint32_t reg4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -258,11 +259,14 @@ struct StepSmem {
     static constexpr int rows = 8 * NT;
     static constexpr uint32_t ring = 0;
     static constexpr uint32_t scales = kStepWarps * kStepStages * kStepStageBytes;     // 64 bytes a stage and warp
-    static constexpr uint32_t q = scales + kStepWarps * kStepStages * 64;              // q~ high, then low parts
-    static constexpr uint32_t ml = q + 2 * rows * kHD * 2;                             // [warp][rows] m, then l
-    static constexpr uint32_t fin = ml + 2 * kStepWarps * rows * 4;                    // [rows] M, then L
-    static constexpr uint32_t misc = fin + 2 * rows * 4;
+    static constexpr uint32_t q = scales + kStepWarps * kStepStages * 64;              // q~ in FP16
+    static constexpr uint32_t ml = q + rows * kHD * 2;                                 // [warp][rows] m, then l
+    static constexpr uint32_t fin = ml + 2 * kStepWarps * rows * 4;                    // [rows] output scale
+    static constexpr uint32_t inv = (fin + rows * 4 + 15) / 16 * 16;                   // rotation frequencies
+    static constexpr uint32_t misc = inv + 64 * 8;
     static constexpr uint32_t total = misc + 16;
+    // a warp's part of a pair, kept in the ring stage it has just read
+    static_assert(rows * kHD * 4 <= kStepStageBytes, "a warp's output fits a stage");
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
 
@@ -271,6 +275,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     using S = StepSmem<NT>;
     using TL = StepTile<FP8>;
     constexpr int kSub = FP8 ? 2 : 1;                    // 16-position parts of a warp's block
+    constexpr int kRowBytes = FP8 ? kHD : 2 * kHD;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -283,8 +288,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
-    float* s_M = reinterpret_cast<float*>(smem + S::fin);
-    float* s_L = s_M + S::rows;
+    float* s_fin = reinterpret_cast<float*>(smem + S::fin);
+    double* s_inv = reinterpret_cast<double*>(smem + S::inv);
     int* s_last = reinterpret_cast<int*>(smem + S::misc);
 
     const float mq = warp_max_abs128(p.q_norm_w);        // an input, not the plan's: before the wait
@@ -293,99 +298,109 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const float qscale = ldexpf(1.f, eq);
     griddep_wait();
 
+    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.sprefix);
     PagedShare share;
-    if (!paged_share_begin(share, hdr->step, reinterpret_cast<const PagedGroup*>(p.ws + L.sgroups),
-                           reinterpret_cast<const long long*>(p.ws + L.sprefix), ng, blockIdx.x, gridDim.x))
+    if (!paged_share_begin(share, hdr->step, reinterpret_cast<const PagedGroup*>(p.ws + L.sgroups), prefix, ng, blockIdx.x,
+                           gridDim.x))
         return;
 
+    // ---- loading.  The stream of tiles runs across pairs: the cursor (f_*)
+    // is two tiles ahead of the one being multiplied, in the next pair if need
+    // be, so that a pair's end does not drain the ring.
     const uint32_t ring = sb + S::ring + warp * (kStepStages * kStepStageBytes) + lane * 16;
     const uint32_t srow = sb + S::scales + warp * (kStepStages * 64);
     const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
     const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
-    constexpr int kRowBytes = FP8 ? kHD : 2 * kHD;
     const int slot_mask = (1 << c.ps_log2) - 1;
-
-    PagedSeg sg;
-    while (paged_share_next(share, sg)) {
-        const PagedGroup& grp = sg.g;
-        const int head = sg.head, t0 = sg.t0, t1 = sg.t1;
-        const int len = c.len[grp.b], row_b = c.cu[grp.b];
-        const int p0 = len + grp.row0;                   // position of the group's first row
-        const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-        const int hi = p0 + grp.nrows;                   // one past the last key any row sees
-        const int key_base = (lo & ~15) + warp * TL::block;
-        const int* table = c.table + (size_t)grp.b * c.max_pages;
-
-        // Page of a 16-position part; -1 where none of it is needed.
-        auto page_of = [&](int key) -> int {
-            return key < hi && key + 16 > lo ? __ldg(table + (key >> c.ps_log2)) : -1;
-        };
-        auto issue = [&](int tile, int stage, const int* pg) {
+    PagedShare f_share = share;
+    int f_left = 0, f_key = 0, f_lo = 0, f_hi = 0, f_head = 0;   // tiles left in its pair; its warp's next key; what is seen
+    const int* f_table = nullptr;
+    int pg[kSub];                                        // pages of its next tile
+    auto see = [&](const PagedGroup& g, int* lo, int* hi) {
+        *lo = p.window > 0 ? max(0, g.p0 - p.window + 1) : 0;
+        *hi = g.p0 + g.nrows;
+    };
+    auto fetch_pages = [&]() {
+#pragma unroll
+        for (int u = 0; u < kSub; ++u) {
+            const int key = f_key + 16 * u;
+            pg[u] = key < f_hi && key + 16 > f_lo ? __ldg(f_table + (key >> c.ps_log2)) : -1;
+        }
+    };
+    auto next_pair = [&]() {
+        PagedSeg s;
+        if (!paged_share_next(f_share, s, false)) return;
+        see(s.g, &f_lo, &f_hi);
+        f_left = s.t1 - s.t0;
+        f_head = s.head;
+        f_key = (f_lo & ~15) + s.t0 * TL::tile + warp * TL::block;
+        f_table = c.table + (size_t)s.g.b * c.max_pages;
+        fetch_pages();
+    };
+    const int koff = j * kRowBytes + i * 16, voff = 2 * i * kRowBytes + j * 16;
+    auto issue = [&](int stage) {
+        if (f_left > 0) {
             const uint32_t dst = ring + stage * kStepStageBytes;
 #pragma unroll
             for (int u = 0; u < kSub; ++u) {
-                const int key = key_base + tile * TL::tile + 16 * u;
-                int page = pg[u];
-                if (page < 0 || page >= c.num_pages) {
-                    if (key < hi && key + 16 > lo && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
-                    page = -1;
-                }
-                const bool live = page >= 0;
-                const size_t row = live ? paged_row(c, page, head, key & slot_mask) : 0;
-                // rows outside [lo, hi) are not read: their slots may hold anything
-                auto on = [&](int r) { return live && key + r >= lo && key + r < hi; };
-                const uint8_t* kr = kp + row * kRowBytes;
-                const uint8_t* vr = vp + row * kRowBytes;
-                if constexpr (!FP8) {
+                const int key = f_key + 16 * u;
+                const bool live = pg[u] >= 0 && pg[u] < c.num_pages;
+                if (!live && key < f_hi && key + 16 > f_lo && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
+                const size_t row = live ? paged_row(c, pg[u], f_head, key & slot_mask) : 0;
+                const uint8_t* kr = kp + row * kRowBytes + koff;
+                const uint8_t* vr = vp + row * kRowBytes + voff;
+                if (live && key >= f_lo && key + 16 <= f_hi) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int r = j + (x >> 2) * 8;
-                        cp16(dst + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 3) * 4 + i) * 16 : 0), on(r));
-                    }
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int r = 2 * i + (x & 1) + ((x >> 1) & 1) * 8;
-                        cp16(dst + 4096 + x * 512, vr + (on(r) ? r * kRowBytes + (x >> 2) * 128 + j * 16 : 0), on(r));
+                    for (int x = 0; x < (FP8 ? 4 : 8); ++x) {
+                        if constexpr (FP8) {
+                            cp16(dst + u * 4096 + x * 512, kr + (x >> 1) * 8 * kRowBytes + (x & 1) * 64, true);
+                            cp16(dst + u * 4096 + 2048 + x * 512, vr + ((x & 1) + (x >> 1) * 8) * kRowBytes, true);
+                        } else {
+                            cp16(dst + x * 512, kr + (x >> 2) * 8 * kRowBytes + (x & 3) * 64, true);
+                            cp16(dst + 4096 + x * 512, vr + ((x & 1) + ((x >> 1) & 1) * 8) * kRowBytes + (x >> 2) * 128, true);
+                        }
                     }
                 } else {
+                    // rows outside [lo, hi) are not read: their slots may hold anything
+                    auto on = [&](int r) { return live && key + r >= f_lo && key + r < f_hi; };
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int r = j + (x >> 1) * 8;
-                        cp16(dst + u * 4096 + x * 512, kr + (on(r) ? r * kRowBytes + ((x & 1) * 4 + i) * 16 : 0), on(r));
+                    for (int x = 0; x < (FP8 ? 4 : 8); ++x) {
+                        const int kx = FP8 ? (x >> 1) * 8 : (x >> 2) * 8;
+                        const int vx = (x & 1) + ((x >> 1) & 1) * 8;
+                        const bool k_on = on(j + kx), v_on = on(2 * i + vx);
+                        const uint8_t* ks = kr + kx * kRowBytes + (FP8 ? (x & 1) : (x & 3)) * 64;
+                        const uint8_t* vs = vr + vx * kRowBytes + (FP8 ? 0 : (x >> 2) * 128);
+                        cp16(dst + (FP8 ? u * 4096 : 0) + x * 512, k_on ? ks : kp, k_on);
+                        cp16(dst + (FP8 ? u * 4096 + 2048 : 4096) + x * 512, v_on ? vs : vp, v_on);
                     }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int r = 2 * i + (x & 1) + (x >> 1) * 8;
-                        cp16(dst + u * 4096 + 2048 + x * 512, vr + (on(r) ? r * kRowBytes + j * 16 : 0), on(r));
-                    }
-                    if (lane < 2) cp16(srow + stage * 64 + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + row, live);
                 }
+                if (FP8 && lane < 2) cp16(srow + stage * 64 + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + row, live);
             }
-            cp_commit();
-        };
-        int pg[kSub];
-        const int n_it = t1 - t0;
-        // the first stages on their way before the queries
-#pragma unroll
-        for (int s = 0; s < kStepStages - 1; ++s) {
-            if (s < n_it) {
-#pragma unroll
-                for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + s) * TL::tile + 16 * u);
-                issue(t0 + s, s, pg);
-            } else {
-                cp_commit();
-            }
+            f_key += TL::tile;
+            if (--f_left > 0) fetch_pages();
+            else next_pair();
         }
+        cp_commit();
+    };
+    next_pair();
 #pragma unroll
-        for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + kStepStages - 1) * TL::tile + 16 * u);
+    for (int s = 0; s < kStepStages - 1; ++s) issue(s);
+    if (p.use_rope && tid < 64) s_inv[tid] = reinterpret_cast<const double*>(p.ws + L.inv)[tid];
+
+    int stage = 0;
+    PagedSeg sg;
+    for (bool first = true; paged_share_next(share, sg, first); first = false) {
+        const int head = sg.head, p0 = sg.g.p0, nrows = sg.g.nrows;
+        int lo, hi;
+        see(sg.g, &lo, &hi);
+        __syncthreads();                                 // s_inv; the last pair's q~ is read
 
         // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
         if (warp < 2 * NT) {
             const int nt = warp >> 1, sub = lane & 7, hh = 4 * (warp & 1) + (lane >> 3);
-            const bool have = nt < grp.nrows;
+            const bool have = nt < nrows;
             const int pos = p0 + (have ? nt : 0);
-            const __nv_bfloat16* src =
-                p.q + ((size_t)(row_b + grp.row0 + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
+            const __nv_bfloat16* src = p.q + ((size_t)(sg.g.row + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
             const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * sub);
             const uint4 b = *reinterpret_cast<const uint4*>(src + 64 + 8 * sub);
             float x0[8], x1[8], ss = 0.f;
@@ -399,17 +414,16 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             ss += __shfl_xor_sync(0xffffffffu, ss, 1);
             ss += __shfl_xor_sync(0xffffffffu, ss, 2);
             ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-            const float rn = qscale / sqrtf(ss * (1.f / kHD) + p.eps);
+            const float rn = qscale * rsqrtf(ss * (1.f / kHD) + p.eps);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x0[e] *= rn * p.q_norm_w[8 * sub + e];
                 x1[e] *= rn * p.q_norm_w[64 + 8 * sub + e];
             }
             if (p.use_rope) {
-                const double* inv = reinterpret_cast<const double*>(p.ws + L.inv);
                 float c0, s0, c1, s1;
-                rope_cos_sin_exact(pos, inv[2 * lane], &c0, &s0);
-                rope_cos_sin_exact(pos, inv[2 * lane + 1], &c1, &s1);
+                rope_cos_sin(pos, s_inv[2 * lane], &c0, &s0);
+                rope_cos_sin(pos, s_inv[2 * lane + 1], &c1, &s1);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int f = 8 * sub + e;
@@ -420,35 +434,31 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     x1[e] = y1;
                 }
             }
-            __half* qh = reinterpret_cast<__half*>(smem + S::q) + (nt * kGroup + hh) * kHD + 8 * sub;
-            __half* ql = qh + S::rows * kHD;
+            uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!have) x0[e] = x1[e] = 0.f;
-                const __half h0 = __float2half_rn(x0[e]), h1 = __float2half_rn(x1[e]);
-                qh[e] = h0;
-                qh[64 + e] = h1;
-                ql[e] = __float2half_rn(x0[e] - __half2float(h0));
-                ql[64 + e] = __float2half_rn(x1[e] - __half2float(h1));
+            for (int e = 0; e < 4; ++e) {
+                h[e] = have ? pack2_f16(x0[2 * e], x0[2 * e + 1]) : 0u;
+                h[4 + e] = have ? pack2_f16(x1[2 * e], x1[2 * e + 1]) : 0u;
             }
+            uint8_t* qd = smem + S::q + ((nt * kGroup + hh) * kHD + 8 * sub) * 2;
+            *reinterpret_cast<uint4*>(qd) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(qd + 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         __syncthreads();
-        // B fragments of q~ (head j, the lane's channels): [high, low][NT][16]
-        uint32_t qf[2][NT][16];
+        // B fragments of q~ (head j, the lane's channels)
+        uint32_t qf[NT][16];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    // 16-bit: chunk 4 x + i of 8 channels; 8-bit: the x % 2 half of chunk 4 (x / 2) + i of 16
-                    const int ch = FP8 ? ((x >> 1) * 4 + i) * 16 + (x & 1) * 8 : (x * 4 + i) * 8;
-                    const uint4 v = lds16(sb + S::q + ((pt * S::rows + nt * kGroup + j) * kHD + ch) * 2);
-                    qf[pt][nt][4 * x] = v.x;
-                    qf[pt][nt][4 * x + 1] = v.y;
-                    qf[pt][nt][4 * x + 2] = v.z;
-                    qf[pt][nt][4 * x + 3] = v.w;
-                }
+            for (int x = 0; x < 4; ++x) {
+                // 16-bit: chunk 4 x + i of 8 channels; 8-bit: the x % 2 half of chunk 4 (x / 2) + i of 16
+                const int ch = FP8 ? ((x >> 1) * 4 + i) * 16 + (x & 1) * 8 : (x * 4 + i) * 8;
+                const uint4 v = lds16(sb + S::q + ((nt * kGroup + j) * kHD + ch) * 2);
+                qf[nt][4 * x] = v.x;
+                qf[nt][4 * x + 1] = v.y;
+                qf[nt][4 * x + 2] = v.z;
+                qf[nt][4 * x + 3] = v.w;
+            }
 
         // ---- the stream
         float acc[NT][8][4], m[NT][2], l[NT][2];
@@ -459,202 +469,188 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
         }
-        int stage = 0;
-        for (int it = 0; it < n_it; ++it) {
-            // the stage after next, into the buffer read in the last iteration
-            if (it + kStepStages - 1 < n_it) {
-                int st2 = stage + kStepStages - 1;
-                if (st2 >= kStepStages) st2 -= kStepStages;
-                issue(t0 + it + kStepStages - 1, st2, pg);
-#pragma unroll
-                for (int u = 0; u < kSub; ++u) pg[u] = page_of(key_base + (t0 + it + kStepStages) * TL::tile + 16 * u);
-            } else {
-                cp_commit();
-            }
+        int key0 = (lo & ~15) + sg.t0 * TL::tile + warp * TL::block;
+        for (int it = sg.t0; it < sg.t1; ++it, key0 += TL::tile) {
+            // the tile after next, into the buffer read in the last iteration
+            issue(stage >= 1 ? stage - 1 : kStepStages - 1);
             cp_wait<kStepStages - 1>();
             if (FP8) __syncwarp();                        // the scales were fetched by other lanes
             const uint32_t src = ring + stage * kStepStageBytes;
-            const int key0 = key_base + (t0 + it) * TL::tile;
-            if (key0 < hi && key0 + TL::block > lo) {
-                // scores: s[u][nt][0..3] = (key j, heads 2i, 2i + 1), (key j + 8, the same)
-                float s[kSub][NT][4];
-                float ev[kSub][2];
+            const uint8_t* ssc = smem + S::scales + (warp * kStepStages + stage) * 64;
+            if (++stage == kStepStages) stage = 0;
+            if (key0 >= hi || key0 + TL::block <= lo) continue;
+            // scores: s[u][nt][0..3] = (key j, heads 2i, 2i + 1), (key j + 8, the same)
+            float s[kSub][NT][4];
+            float ev[kSub][2];
 #pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    float sl[NT][4];
+            for (int u = 0; u < kSub; ++u) {
+                float s2[NT][4];                          // two chains of products
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[u][nt][e] = sl[nt][e] = 0.f;
-                    if constexpr (!FP8) {
+                    for (int e = 0; e < 4; ++e) s[u][nt][e] = s2[nt][e] = 0.f;
+                if constexpr (!FP8) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint4 a = lds16(src + x * 512), b = lds16(src + (4 + x) * 512);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma_f16(s[u][nt], a.x, b.x, a.y, b.y, qf[0][nt][4 * x], qf[0][nt][4 * x + 1]);
-                                mma_f16(sl[nt], a.x, b.x, a.y, b.y, qf[1][nt][4 * x], qf[1][nt][4 * x + 1]);
-                                mma_f16(s[u][nt], a.z, b.z, a.w, b.w, qf[0][nt][4 * x + 2], qf[0][nt][4 * x + 3]);
-                                mma_f16(sl[nt], a.z, b.z, a.w, b.w, qf[1][nt][4 * x + 2], qf[1][nt][4 * x + 3]);
-                            }
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) s[u][nt][e] = (s[u][nt][e] + sl[nt][e]) * C;
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint4 a = lds16(src + u * 4096 + x * 512), b = lds16(src + u * 4096 + (2 + x) * 512);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint32_t aw = reg4(a, r), bw = reg4(b, r);
-                                const uint32_t a0 = e4m3_f16(aw & 0xffffu), a2 = e4m3_f16(aw >> 16);
-                                const uint32_t a1 = e4m3_f16(bw & 0xffffu), a3 = e4m3_f16(bw >> 16);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const int f = 8 * x + 2 * r;
-                                    mma_f16(s[u][nt], a0, a1, a2, a3, qf[0][nt][f], qf[0][nt][f + 1]);
-                                    mma_f16(sl[nt], a0, a1, a2, a3, qf[1][nt][f], qf[1][nt][f + 1]);
-                                }
-                            }
-                        }
-                        const uint8_t* ssc = smem + S::scales + (warp * kStepStages + stage) * 64 + u * 32;
-                        const float k0 = paged_scale(ssc[j]) * C, k1 = paged_scale(ssc[j + 8]) * C;
-                        ev[u][0] = (float)((int)ssc[16 + j] - 127);
-                        ev[u][1] = (float)((int)ssc[24 + j] - 127);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                s[u][nt][e] = fmaf(s[u][nt][e] + sl[nt][e], e < 2 ? k0 : k1, ev[u][e >> 1]);
-                    }
-                }
-                // masks: only where some row does not see the whole block
-                if (key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window)) {
-#pragma unroll
-                    for (int u = 0; u < kSub; ++u) {
+                    for (int x = 0; x < 4; ++x) {
+                        const uint4 a = lds16(src + x * 512), b = lds16(src + (4 + x) * 512);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const int pos = p0 + nt, wl = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int k = key0 + 16 * u + j + (e >> 1) * 8;
-                                if (k > pos || k < wl) s[u][nt][e] = -INFINITY;
-                            }
-                        }
-                        // slots that hold no key of this call have any scale
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int k = key0 + 16 * u + j + 8 * e;
-                            if (k < lo || k >= hi) ev[u][e] = 0.f;
+                            mma_f16(s[u][nt], a.x, b.x, a.y, b.y, qf[nt][4 * x], qf[nt][4 * x + 1]);
+                            mma_f16(s2[nt], a.z, b.z, a.w, b.w, qf[nt][4 * x + 2], qf[nt][4 * x + 3]);
                         }
                     }
-                }
-                // raise the running max where a score passes it by 2^8
-                bool up = false;
-#pragma unroll
-                for (int u = 0; u < kSub; ++u)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) up = up || s[u][nt][e] > m[nt][e & 1] + 8.f;
-                if (__any_sync(0xffffffffu, up)) {
+                        for (int e = 0; e < 4; ++e) s[u][nt][e] = (s[u][nt][e] + s2[nt][e]) * C;
+                } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float mx = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
-                            if (kSub == 2) mx = fmaxf(mx, fmaxf(s[kSub - 1][nt][h], s[kSub - 1][nt][2 + h]));
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            const float mn = fmaxf(m[nt][h], mx);
-                            const float al = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - mn) : 0.f;
-                            m[nt][h] = mn;
-                            l[nt][h] *= al;
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                acc[nt][x][h] *= al;
-                                acc[nt][x][2 + h] *= al;
-                            }
-                        }
-                }
-#pragma unroll
-                for (int u = 0; u < kSub; ++u) {
-                    uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float pr[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float mm = m[nt][e & 1];
-                            pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm : 0.f));
-                        }
-                        if constexpr (!FP8) {
-                            l[nt][0] += pr[0] + pr[2];
-                            l[nt][1] += pr[1] + pr[3];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t h = pack2_bf16(pr[2 * e], pr[2 * e + 1]);
-                                ph[nt][e] = transpose8(h);
-                                pl[nt][e] = transpose8(pack2_bf16(pr[2 * e] - __uint_as_float(h << 16),
-                                                                  pr[2 * e + 1] - __uint_as_float(h & 0xffff0000u)));
-                            }
-                        } else {
-                            // l in units of 2^m: the scale's exponent taken back
-                            const float i0 = __uint_as_float((uint32_t)(127 - (int)ev[u][0]) << 23);
-                            const float i1 = __uint_as_float((uint32_t)(127 - (int)ev[u][1]) << 23);
-                            l[nt][0] += pr[0] * i0 + pr[2] * i1;
-                            l[nt][1] += pr[1] * i0 + pr[3] * i1;
-                            ph[nt][0] = transpose8(pack2_f16(pr[0], pr[1]));
-                            ph[nt][1] = transpose8(pack2_f16(pr[2], pr[3]));
-                        }
-                    }
-                    if constexpr (!FP8) {
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh) {
-                            const uint4 v0 = lds16(src + 4096 + (hh * 4 + 0) * 512), v1 = lds16(src + 4096 + (hh * 4 + 1) * 512);
-                            const uint4 v2 = lds16(src + 4096 + (hh * 4 + 2) * 512), v3 = lds16(src + 4096 + (hh * 4 + 3) * 512);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint32_t a0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5410);
-                                const uint32_t a1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7632);
-                                const uint32_t a2 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5410);
-                                const uint32_t a3 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7632);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                                    mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
-                                }
-                            }
-                        }
-                    } else {
-                        const uint32_t vs = src + u * 4096 + 2048;
-                        const uint4 v0 = lds16(vs), v1 = lds16(vs + 512), v2 = lds16(vs + 1024), v3 = lds16(vs + 1536);
+                    for (int x = 0; x < 2; ++x) {
+                        const uint4 a = lds16(src + u * 4096 + x * 512), b = lds16(src + u * 4096 + (2 + x) * 512);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const uint32_t x0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5140);
-                            const uint32_t x1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7362);
-                            const uint32_t y0 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5140);
-                            const uint32_t y1 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7362);
+                            const uint32_t aw = reg4(a, r), bw = reg4(b, r);
+                            const uint32_t a0 = e4m3_f16(aw), a2 = e4m3_f16(aw >> 16);
+                            const uint32_t a1 = e4m3_f16(bw), a3 = e4m3_f16(bw >> 16);
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const uint32_t xx = hf ? x1 : x0, yy = hf ? y1 : y0;
-                                const uint32_t a0 = e4m3_f16(xx & 0xffffu), a1 = e4m3_f16(xx >> 16);
-                                const uint32_t a2 = e4m3_f16(yy & 0xffffu), a3 = e4m3_f16(yy >> 16);
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16((r & 1) ? s2[nt] : s[u][nt], a0, a1, a2, a3, qf[nt][8 * x + 2 * r], qf[nt][8 * x + 2 * r + 1]);
+                        }
+                    }
+                    const float k0 = paged_scale(ssc[u * 32 + j]) * C, k1 = paged_scale(ssc[u * 32 + j + 8]) * C;
+                    ev[u][0] = (float)((int)ssc[u * 32 + 16 + j] - 127);
+                    ev[u][1] = (float)((int)ssc[u * 32 + 24 + j] - 127);
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma_f16(acc[nt][2 * r + hf], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[u][nt][e] = fmaf(s[u][nt][e] + s2[nt][e], e < 2 ? k0 : k1, ev[u][e >> 1]);
+                }
+            }
+            // masks: only where some row does not see the whole block
+            if (key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window)) {
+#pragma unroll
+                for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int pos = p0 + nt, wl = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = key0 + 16 * u + j + (e >> 1) * 8;
+                            if (k > pos || k < wl) s[u][nt][e] = -INFINITY;
+                        }
+                    }
+                    // slots that hold no key of this call have any scale
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = key0 + 16 * u + j + 8 * e;
+                        if (k < lo || k >= hi) ev[u][e] = 0.f;
+                    }
+                }
+            }
+            // raise the running max where a score passes it by 2^8
+            bool up = false;
+#pragma unroll
+            for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) up = up || fmaxf(s[u][nt][e], s[u][nt][2 + e]) > m[nt][e] + 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float mx = fmaxf(s[0][nt][h], s[0][nt][2 + h]);
+                        if (kSub == 2) mx = fmaxf(mx, fmaxf(s[kSub - 1][nt][h], s[kSub - 1][nt][2 + h]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const float mn = fmaxf(m[nt][h], mx);
+                        const float al = m[nt][h] > -INFINITY ? st_ex2(m[nt][h] - mn) : 0.f;
+                        m[nt][h] = mn;
+                        l[nt][h] *= al;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            acc[nt][x][h] *= al;
+                            acc[nt][x][2 + h] *= al;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < kSub; ++u) {
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float pr[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float mm = m[nt][e & 1];
+                        pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm : 0.f));
+                    }
+                    if constexpr (!FP8) {
+                        l[nt][0] += pr[0] + pr[2];
+                        l[nt][1] += pr[1] + pr[3];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t h = pack2_bf16(pr[2 * e], pr[2 * e + 1]);
+                            ph[nt][e] = transpose8(h);
+                            pl[nt][e] = transpose8(pack2_bf16(pr[2 * e] - __uint_as_float(h << 16),
+                                                              pr[2 * e + 1] - __uint_as_float(h & 0xffff0000u)));
+                        }
+                    } else {
+                        // l in units of 2^m: the scale's exponent taken back
+                        const float i0 = __uint_as_float((uint32_t)(127 - (int)ev[u][0]) << 23);
+                        const float i1 = __uint_as_float((uint32_t)(127 - (int)ev[u][1]) << 23);
+                        l[nt][0] += pr[0] * i0 + pr[2] * i1;
+                        l[nt][1] += pr[1] * i0 + pr[3] * i1;
+                        ph[nt][0] = transpose8(pack2_f16(pr[0], pr[1]));
+                        ph[nt][1] = transpose8(pack2_f16(pr[2], pr[3]));
+                    }
+                }
+                if constexpr (!FP8) {
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const uint4 v0 = lds16(src + 4096 + (hh * 4 + 0) * 512), v1 = lds16(src + 4096 + (hh * 4 + 1) * 512);
+                        const uint4 v2 = lds16(src + 4096 + (hh * 4 + 2) * 512), v3 = lds16(src + 4096 + (hh * 4 + 3) * 512);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const uint32_t a0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5410);
+                            const uint32_t a1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7632);
+                            const uint32_t a2 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5410);
+                            const uint32_t a3 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7632);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                                mma_bf16(acc[nt][hh * 4 + r], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
                             }
+                        }
+                    }
+                } else {
+                    const uint32_t vs = src + u * 4096 + 2048;
+                    const uint4 v0 = lds16(vs), v1 = lds16(vs + 512), v2 = lds16(vs + 1024), v3 = lds16(vs + 1536);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t x0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5140);
+                        const uint32_t x1 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x7362);
+                        const uint32_t y0 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x5140);
+                        const uint32_t y1 = __byte_perm(reg4(v2, r), reg4(v3, r), 0x7362);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const uint32_t xx = hf ? x1 : x0, yy = hf ? y1 : y0;
+                            const uint32_t a0 = e4m3_f16(xx), a1 = e4m3_f16(xx >> 16);
+                            const uint32_t a2 = e4m3_f16(yy), a3 = e4m3_f16(yy >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16(acc[nt][2 * r + hf], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
                         }
                     }
                 }
             }
-            if (++stage == kStepStages) stage = 0;
         }
-        cp_wait<0>();
 
-        // ---- the four warps' states into one, in warp order
+        // ---- the four warps' states into one, in warp order.  A warp's part
+        // goes where it read its last tile; the two tiles on their way for the
+        // next pair are in the other stages.
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -666,8 +662,11 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     s_l[warp * S::rows + nt * kGroup + 2 * i + h] = l[nt][h];
                 }
             }
-        __syncthreads();                                  // every warp's ring is drained, too
-        float* buf = reinterpret_cast<float*>(smem + S::ring) + warp * S::rows * kHD;
+        __syncthreads();
+        const int used = stage == 0 ? kStepStages - 1 : stage - 1;
+        float* bufs = reinterpret_cast<float*>(smem + S::ring + used * kStepStageBytes);
+        constexpr int kBufStep = kStepStages * kStepStageBytes / 4;       // floats between two warps' stages
+        float* buf = bufs + warp * kBufStep;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -683,7 +682,10 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     *reinterpret_cast<float2*>(buf + row * kHD + ch) = make_float2(acc[nt][x][h] * a, acc[nt][x][2 + h] * a);
                 }
             }
-        if (tid < S::rows) {
+        const int rows = kGroup * nrows;
+        const size_t out_row = (size_t)sg.g.row;
+        float* dst = part + (2 * (size_t)blockIdx.x + (sg.first ? 0 : 1)) * kStepPart;   // where the pair is held in part
+        if (tid < rows) {
             float M = s_m[tid], l4 = 0.f;
 #pragma unroll
             for (int w = 1; w < kStepWarps; ++w) M = fmaxf(M, s_m[w * S::rows + tid]);
@@ -692,82 +694,121 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 const float mw = s_m[w * S::rows + tid];
                 l4 += s_l[w * S::rows + tid] * (mw > -INFINITY ? st_ex2(mw - M) : 0.f);
             }
-            s_M[tid] = M;
-            s_L[tid] = l4;
+            if (sg.whole) {
+                const int h = kGroup * head + (tid & 7);
+                float v;
+                paged_finish(M, l4, p.sinks[h], &s_fin[tid], &v);
+                if (p.lse) p.lse[(size_t)h * c.T + out_row + (tid >> 3)] = v;
+            } else {
+                dst[tid] = M;
+                dst[kPagedStepRows + tid] = l4;
+            }
         }
         __syncthreads();
-        const float* b0 = reinterpret_cast<const float*>(smem + S::ring) + tid;
-        const int rows = kGroup * grp.nrows;
-        const size_t out_row = (size_t)(row_b + grp.row0);
-        if (sg.whole) {
-            for (int r = 0; r < rows; ++r) {
-                float o = 0.f, v;
+        // warp w: rows w, w + 4, ..; a lane four channels
 #pragma unroll
-                for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
-                const int h = kGroup * head + (r & 7);
-                float sc;
-                paged_finish(s_M[r], s_L[r], p.sinks[h], &sc, &v);
-                o *= sc;
-                const size_t tr = out_row + (r >> 3);
-                p.out[(tr * nh + h) * kHD + tid] = __float2bfloat16_rn(o);
-                if (tid == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
-            }
-            __syncthreads();
-            continue;
-        }
-        {
-            // slot 2 c: the CTA's first segment, 2 c + 1: a later one (its last)
-            float* dst = part + (2 * (size_t)blockIdx.x + (sg.first ? 0 : 1)) * kStepPart;
-            if (tid < S::rows) {
-                dst[tid] = s_M[tid];
-                dst[16 + tid] = s_L[tid];
-            }
-            for (int r = 0; r < rows; ++r) {
-                float o = 0.f;
+        for (int r0 = 0; r0 < S::rows; r0 += kStepWarps) {
+            const int r = r0 + warp;
+            if (r >= rows) break;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kStepWarps; ++w) o += b0[(w * S::rows + r) * kHD];
-                dst[32 + r * kHD + tid] = o;
+            for (int w = 0; w < kStepWarps; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(bufs + w * kBufStep + r * kHD + 4 * lane);
+                o.x += v.x;
+                o.y += v.y;
+                o.z += v.z;
+                o.w += v.w;
+            }
+            if (sg.whole) {
+                const float sc = s_fin[r];
+                *reinterpret_cast<uint2*>(p.out + ((out_row + (r >> 3)) * nh + kGroup * head + (r & 7)) * kHD + 4 * lane) =
+                    make_uint2(pack2_bf16(o.x * sc, o.y * sc), pack2_bf16(o.z * sc, o.w * sc));
+            } else {
+                *reinterpret_cast<float4*>(dst + 2 * kPagedStepRows + r * kHD + 4 * lane) = o;
             }
         }
-        // CTAs that hold a part of this segment: the owners of its first and last tile and all between
-        const long long cf = paged_owner(share.W, share.G, sg.seg), cl = paged_owner(share.W, share.G, sg.seg + grp.tiles - 1);
+        if (sg.whole) continue;                          // the next pair begins with a barrier
+
+        // ---- the last of the pair's CTAs to finish folds their parts in CTA order
+        const PagedParts pp = paged_parts(hdr->step, prefix, sg, ng, gridDim.x);
         __threadfence();
         __syncthreads();
-        if (tid == 0) *s_last = atomicAdd(arrive + (size_t)sg.gi * ng + head, 1) == (int)(cl - cf);
+        if (tid == 0) *s_last = atomicAdd(arrive + (size_t)sg.gi * ng + head, 1) == pp.cl - pp.cf;
         __syncthreads();
         if (*s_last) {
             __threadfence();
-            for (int r = warp; r < rows; r += kStepWarps) {
-                float M = -INFINITY;
-                auto slot = [&](long long x) { return part + paged_slot(share.W, share.G, sg.seg, x) * kStepPart; };
-                for (long long x = cf + lane; x <= cl; x += 32) M = fmaxf(M, __ldcg(slot(x) + r));
+            // warp w adds CTAs cf + w, + 4, .. (every row: independent loads),
+            // the warps meet in the buffers above
+            float M[S::rows / 8], Ls[S::rows / 8];        // lane: row lane / 4 (+ 8), of CTAs lane % 4, + 4, ..
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                float Ls = 0.f;
-                float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                for (long long x = cf; x <= cl; ++x) {
-                    const float* s = slot(x);
-                    const float ms = __ldcg(s + r), ls = __ldcg(s + 16 + r);
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + 32 + r * kHD) + lane);
-                    const float a = ms > -INFINITY ? exp2f(ms - M) : 0.f;
-                    Ls += ls * a;
-                    o4.x += v.x * a;
-                    o4.y += v.y * a;
-                    o4.z += v.z * a;
-                    o4.w += v.w * a;
+            for (int x = 0; x < S::rows / 8; ++x) M[x] = -INFINITY;
+            for (int y = pp.cf + i; y <= pp.cl; y += 4)
+#pragma unroll
+                for (int x = 0; x < S::rows / 8; ++x)
+                    if (j + 8 * x < rows) M[x] = fmaxf(M[x], __ldcg(part + pp.slot(y) * kStepPart + j + 8 * x));
+#pragma unroll
+            for (int x = 0; x < S::rows / 8; ++x) {
+                M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], 1));
+                M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], 2));
+                Ls[x] = 0.f;
+            }
+            float4 o[S::rows];
+#pragma unroll
+            for (int r = 0; r < S::rows; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = pp.cf + warp; y <= pp.cl; y += kStepWarps) {
+                const float* b = part + pp.slot(y) * kStepPart;
+                float a[S::rows / 8];
+#pragma unroll
+                for (int x = 0; x < S::rows / 8; ++x) {
+                    a[x] = 0.f;
+                    if (j + 8 * x < rows) {
+                        const float ms = __ldcg(b + j + 8 * x), ls = __ldcg(b + kPagedStepRows + j + 8 * x);
+                        a[x] = ms > -INFINITY ? exp2f(ms - M[x]) : 0.f;
+                        Ls[x] += ls * a[x];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < S::rows; ++r) {
+                    if (r >= rows) break;
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(b + 2 * kPagedStepRows + r * kHD) + lane);
+                    const float ar = __shfl_sync(0xffffffffu, a[r >> 3], 4 * (r & 7));
+                    o[r].x += v.x * ar;
+                    o[r].y += v.y * ar;
+                    o[r].z += v.z * ar;
+                    o[r].w += v.w * ar;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < S::rows; ++r) *reinterpret_cast<float4*>(buf + r * kHD + 4 * lane) = o[r];
+            if (i == 0)
+#pragma unroll
+                for (int x = 0; x < S::rows / 8; ++x) {
+                    s_m[warp * S::rows + j + 8 * x] = M[x];
+                    s_l[warp * S::rows + j + 8 * x] = Ls[x];
+                }
+            __syncthreads();
+            for (int r = warp; r < rows; r += kStepWarps) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                float l4 = 0.f;
+#pragma unroll
+                for (int w = 0; w < kStepWarps; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(bufs + w * kBufStep + r * kHD + 4 * lane);
+                    t.x += v.x;
+                    t.y += v.y;
+                    t.z += v.z;
+                    t.w += v.w;
+                    l4 += s_l[w * S::rows + r];
                 }
                 const int h = kGroup * head + (r & 7);
-                const size_t tr = out_row + (r >> 3);
                 float sc, v;
-                paged_finish(M, Ls, p.sinks[h], &sc, &v);
-                *reinterpret_cast<uint2*>(p.out + (tr * nh + h) * kHD + 4 * lane) =
-                    make_uint2(pack2_bf16(o4.x * sc, o4.y * sc), pack2_bf16(o4.z * sc, o4.w * sc));
-                if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + tr] = v;
+                paged_finish(s_m[r], l4, p.sinks[h], &sc, &v);
+                *reinterpret_cast<uint2*>(p.out + ((out_row + (r >> 3)) * nh + h) * kHD + 4 * lane) =
+                    make_uint2(pack2_bf16(t.x * sc, t.y * sc), pack2_bf16(t.z * sc, t.w * sc));
+                if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + out_row + (r >> 3)] = v;
             }
         }
-        __syncthreads();
     }
+    cp_wait<0>();
 }
 
 // ============================================================================ host

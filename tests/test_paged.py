@@ -9,14 +9,13 @@ Tolerances, from the roundings that the kernels make:
   is read back: exact bits.
 * Attention: the output's BF16 rounding (2^-8 relative), and relative to
   A = sum p |V| / Z: the rounding of P and twice the error of the logits.
-  The step kernel keeps q~ to 2^-22 (two FP16 parts) and sums 128 FP32
-  products: a logit is off by at most dz = 2^-20 spread + 4e-6, with spread =
-  max_j sum_c |q~_c K_jc| / sqrt(128) (the constant: the FP32 exponent and
-  the running sums).  P is kept to 2^-16 (two BF16 parts; 8-bit values: 2^-11
-  once, in FP16), its sums and the exponential to 2^-16: 2 dz + 2^-15 of A
-  (8-bit values: + 2^-11).  LSE: dz and an FP32 last place or two of itself.
-  The chunk kernel (a sequence of the call has over 8 new tokens) rounds q~ to
-  FP16 and P to BF16: dz = 2^-11 spread + 2e-5 and 2^-8 + 2 dz of A.
+  q~ is rounded to FP16 (2^-11 relative): a logit is off by at most dz =
+  2^-11 spread + 2e-5, with spread = max_j sum_c |q~_c K_jc| / sqrt(128) (the
+  constant: FP32 sums, the rotation's and the exponential's approximations).
+  The step kernel keeps P to 2^-16 (two BF16 parts; 8-bit values: 2^-11 once,
+  in FP16) and its sums to 2^-16: 2 dz + 2^-15 of A (8-bit values: + 2^-11).
+  The chunk kernel (a sequence of the call has over 8 new tokens) rounds P to
+  BF16: 2 dz + 2^-8 of A.  LSE: dz and an FP32 last place or two of itself.
 """
 import numpy as np
 import pytest
@@ -93,12 +92,9 @@ def check_attend(c, t, out, lse, chunk=False):
     n = c.rows
     got = out.float().cpu().numpy().reshape(c.T, 8 * c.g, 128)[:n].astype(np.float64)
     ref, ab, spread, rl = ref[:n], ab[:n], spread[:n], rl[:, :n]
-    if chunk:
-        dz = 2.0 ** -11 * spread + 2e-5
-        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * dz[..., None]) * ab
-    else:
-        dz = 2.0 ** -20 * spread + 4e-6
-        tol = 2.0 ** -8 * np.abs(ref) + (2 * dz[..., None] + 2.0 ** -15 + (2.0 ** -11 if c.fp8 else 0.0)) * ab
+    dz = 2.0 ** -11 * spread + 2e-5
+    p_off = 2.0 ** -8 if chunk else 2.0 ** -15 + (2.0 ** -11 if c.fp8 else 0.0)
+    tol = 2.0 ** -8 * np.abs(ref) + (2 * dz[..., None] + p_off) * ab
     err = np.abs(got - ref)
     print("rel %.2e" % (np.linalg.norm(err) / max(np.linalg.norm(ref), 1e-300)))
     assert (err <= tol).all()
