@@ -109,23 +109,20 @@ struct PagedGroup {
 };
 
 // The work of one kernel: the tiles of all (group, KV head) pairs in a row,
-// group by group, head by head.  The plan kernel writes the groups and the
-// exclusive prefix of their tile counts (prefix[n] = tiles); CTA c of G takes
-// tiles [W c / G, W (c + 1) / G) of the W = tiles x heads, so every CTA has
-// the same number for any mix of lengths, and holds at most two pairs in part.
+// group by group, head by head.  CTA c of G takes tiles [W c / G, W (c + 1) /
+// G) of the W = tiles x heads, so every CTA has the same number for any mix of
+// lengths, and holds at most two pairs in part.  For the chunk kernel a plan
+// kernel writes the groups and the exclusive prefix of their tile counts
+// (prefix[n] = tiles); the step kernel's CTAs work it out themselves.
 struct PagedList { long long tiles; int n, pad; };
 
 struct PagedPlanHeader {
     int status;                  // device-side status (0 = ok)
     int pad0;
-    PagedList step, chunk;
-    int pad[54];
+    PagedList chunk;
+    int pad[58];
 };
 static_assert(sizeof(PagedPlanHeader) == 256, "plan header");
-
-// What the plan kernel needs to know of a list: sequences of n_min .. n_max
-// new tokens, in groups of nt, whose tiles start at a multiple of align.
-struct PagedListSpec { int n_min, n_max, nt, tile, align; };
 
 constexpr int kChunkTok = 32;            // new tokens of a chunk kernel's group
 constexpr int kPagedStepRows = 16;       // query rows of a step partial
@@ -134,28 +131,37 @@ constexpr int kPagedStepRows = 16;       // query rows of a step partial
 constexpr size_t kStepPart = (size_t)kPagedStepRows * (kHD + 2);
 constexpr size_t kChunkPart = (size_t)8 * kChunkTok * (kHD + 2);
 
-// Workspace of an attention call.  sms: CTAs of the chunk kernel (0: not run).
+// Workspace of an attention call: of the step kernel (chunk_ctas == 0) a flag
+// and two partials a CTA, of the chunk kernel the plan and two partials a CTA.
 struct PagedWs {
-    size_t header, inv, sgroups, sprefix, arrive, spart, cgroups, cprefix, cpart, total;
+    size_t header, flags, spart, inv, groups, prefix, cpart, total;
 };
-__host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas, int chunk_ctas) {
+__host__ __device__ inline PagedWs paged_ws(int B, int T, int step_ctas, int chunk_ctas) {
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.inv = o;     o += 64 * sizeof(double);
-    L.sgroups = o; o = ws_align(o + sizeof(PagedGroup) * (size_t)T, 256);
-    L.sprefix = o; o = ws_align(o + sizeof(long long) * ((size_t)T + 1), 256);
-    L.arrive = o;  o = ws_align(o + sizeof(int) * (size_t)T * ng, 256);
-    L.spart = o;   o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
-    L.cgroups = L.cprefix = L.cpart = o;
-    if (chunk_ctas > 0) {
+    L.flags = L.spart = L.inv = L.groups = L.prefix = L.cpart = o;
+    if (chunk_ctas == 0) {
+        o = ws_align(o + sizeof(int) * (size_t)step_ctas, 256);
+        L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
+    } else {
         const size_t n = (size_t)T / kChunkTok + (B < T ? B : T);
-        L.cgroups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
-        L.cprefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
-        L.cpart = o;   o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
+        o += 64 * sizeof(double);
+        L.groups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
+        L.prefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
+        L.cpart = o;  o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
     }
     L.total = o;
     return L;
+}
+
+// New tokens of the sequence whose packed rows are [a, z) at positions len ..;
+// -1 where its entries are ill-formed.
+__device__ __forceinline__ int paged_new(const PagedCache& c, int max_new, int a, int z, int len) {
+    const int n = z - a;
+    if (a < 0 || z < a || z > c.T || n > max_new || len < 0 || len >= FLINT_MAX_TOKENS) return -1;
+    const long long end = (long long)len + n;
+    return n > 0 && (end > FLINT_MAX_TOKENS || end > ((long long)c.max_pages << c.ps_log2)) ? -1 : n;
 }
 
 // Joins the sink to a row's running state (M, L in log2 units, O in units of
@@ -217,27 +223,20 @@ __device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g, boo
     if (++s.head == s.ng) { s.head = 0; ++s.gi; }
     return true;
 }
-// The first of all W tiles that is pair (gi, head)'s.
-__device__ __forceinline__ long long paged_seg_begin(const long long* prefix, const PagedSeg& g, int ng) {
-    return prefix[g.gi] * ng + (long long)g.head * g.g.tiles;
-}
 // The CTA that owns tile x.
 __device__ __forceinline__ long long paged_owner(long long W, long long G, long long x) { return ((x + 1) * G - 1) / W; }
-// The CTAs cf .. cl that hold parts of a pair, and where they left them: a
-// CTA's first pair in slot 2 c, a later one (its last) in 2 c + 1.  Every CTA
-// but cf begins inside the pair.
+// The CTAs cf .. cl that hold parts of the pair whose first tile is tile seg
+// of all W, and where they left them: a CTA's first pair in slot 2 c, a later
+// one (its last) in 2 c + 1.  Every CTA but cf begins inside the pair.
 struct PagedParts {
     int cf, cl;
     bool second;                 // in cf's share it is not the first pair
     __device__ __forceinline__ size_t slot(int x) const { return 2 * (size_t)x + (x == cf && second ? 1 : 0); }
 };
-__device__ __forceinline__ PagedParts paged_parts(const PagedList& l, const long long* prefix, const PagedSeg& g, int ng,
-                                                  int ctas) {
-    const long long W = l.tiles * ng, G = W < (long long)ctas ? W : (long long)ctas;
-    const long long seg = paged_seg_begin(prefix, g, ng);
+__device__ __forceinline__ PagedParts paged_parts(long long W, long long G, long long seg, int tiles) {
     PagedParts r;
     r.cf = (int)paged_owner(W, G, seg);
-    r.cl = (int)paged_owner(W, G, seg + g.g.tiles - 1);
+    r.cl = (int)paged_owner(W, G, seg + tiles - 1);
     r.second = W * r.cf / G < seg;
     return r;
 }

@@ -126,6 +126,121 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
+// ---------------------------------------------------------------- plan
+// Exclusive prefix of v over the (1,024 threads') block; the block's total in *total.
+template <typename I>
+__device__ __forceinline__ I plan_scan(I v, I* sh, I* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    I x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const I y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sh[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        I w = sh[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const I y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        sh[lane] = w;
+    }
+    __syncthreads();
+    const I r = x - v + (warp ? sh[warp - 1] : 0);
+    *total = sh[31];
+    __syncthreads();
+    return r;
+}
+
+// Sequence b's new tokens; 0 (and *bad) where its entries are ill-formed.
+__device__ __forceinline__ int plan_new(const PagedAttnParams& p, int b, bool* bad) {
+    const int n = paged_new(p.c, p.max_new, p.c.cu[b], p.c.cu[b + 1], p.c.len[b]);
+    if (n < 0) *bad = true;
+    return max(n, 0);
+}
+
+// One block: checks the boundaries and lengths, writes the groups with the
+// exclusive prefix of their chunk counts, and leaves the rotation frequencies.
+// Group offsets of the sequences are kept in shared memory; past kPlanSeqs
+// sequences only every `every`-th is, and the rest is walked.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 4096;
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p) {
+    griddep_launch_dependents();
+    __shared__ int s_bad, sh_i[32], off[kPlanSeqs];
+    __shared__ long long sh_l[32];
+    const int tid = threadIdx.x;
+    const PagedCache& c = p.c;
+    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
+    PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
+    double* inv = reinterpret_cast<double*>(p.ws + L.inv);
+    PagedGroup* groups = reinterpret_cast<PagedGroup*>(p.ws + L.groups);
+    long long* prefix = reinterpret_cast<long long*>(p.ws + L.prefix);
+    if (tid == 0) s_bad = (c.cu[0] != 0 || c.cu[c.B] > c.T) ? 1 : 0;
+    if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
+    __syncthreads();
+    const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
+    int n_groups = 0;
+    for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
+        const int b1 = b0 + tid * every;
+        int cnt = 0;
+        bool bad = false;
+        for (int b = b1; b < min(b1 + every, c.B); ++b) cnt += (plan_new(p, b, &bad) + kChunkTok - 1) / kChunkTok;
+        if (bad) s_bad = 1;
+        int tot;
+        const int ex = plan_scan(cnt, sh_i, &tot);
+        if (b1 < c.B) off[b1 / every] = n_groups + ex;
+        n_groups += tot;
+    }
+    __syncthreads();
+    const int n_off = (c.B + every - 1) / every;
+    long long tiles = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
+        const int g = g0 + tid;
+        PagedGroup r = {};
+        if (g < n_groups) {
+            int lo = 0, hi = n_off - 1;                       // last entry with off <= g
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (off[mid] <= g) lo = mid; else hi = mid - 1;
+            }
+            int at = off[lo];
+            bool bad = false;
+            for (int b = lo * every; b < c.B; ++b) {          // one step where every == 1
+                const int n = plan_new(p, b, &bad), k = (n + kChunkTok - 1) / kChunkTok;
+                if (g < at + k) {
+                    const int row0 = (g - at) * kChunkTok;
+                    r.b = b;
+                    r.nrows = min(kChunkTok, n - row0);
+                    r.p0 = c.len[b] + row0;
+                    r.row = c.cu[b] + row0;
+                    const int first = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
+                    r.tiles = (r.p0 + r.nrows - (first & ~((1 << c.ps_log2) - 1)) + kKeyChunk - 1) / kKeyChunk;
+                    break;
+                }
+                at += k;
+            }
+        }
+        long long tot;
+        const long long ex = plan_scan((long long)r.tiles, sh_l, &tot);
+        if (g < n_groups) {
+            groups[g] = r;
+            prefix[g] = tiles + ex;
+        }
+        tiles += tot;
+    }
+    if (tid == 0) {
+        prefix[n_groups] = tiles;
+        hdr->chunk.n = n_groups;
+        hdr->chunk.tiles = tiles;
+        hdr->status = s_bad ? kStatusInvalid : kStatusOk;
+    }
+}
+
+// ---------------------------------------------------------------- chunk kernel
 // What a group sees of its cache, and its chunks.
 struct PcGroup {
     int p0, hi;          // position of its first row; one past its last row's
@@ -160,7 +275,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int* abort_flag = &misc->abort_flag;
     const PagedCache& c = p.c;
     const int ng = c.ng;
-    const PagedWs L = paged_ws(c.B, c.T, ng, p.step_ctas, p.chunk_ctas);
+    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
     int* status = &hdr->status;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -217,8 +332,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     PagedShare share;
     PagedSeg sg;
     bool first = true;
-    const bool work = paged_share_begin(share, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.cgroups),
-                                        reinterpret_cast<const long long*>(p.ws + L.cprefix), ng, blockIdx.x, gridDim.x);
+    const bool work = paged_share_begin(share, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.groups),
+                                        reinterpret_cast<const long long*>(p.ws + L.prefix), ng, blockIdx.x, gridDim.x);
 
     if (!work) {
         // nothing in flight: straight to the end
@@ -799,6 +914,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!cur.whole) {
                 // partial: m, l and O in FP32, channel quads outermost so that
                 // the rows of a warp are consecutive
+                tc_fence_before();
+                if (kTokPerTile * t + 4 * (warp & 3) >= cur.g.nrows) continue;    // none of the warp's rows is a new token's
                 float* dst = reinterpret_cast<float*>(p.ws + L.cpart) + (2 * (size_t)blockIdx.x + (cur.first ? 0 : 1)) * kChunkPart;
                 const int row = 128 * t + r;
                 dst[row] = m;
@@ -880,18 +997,19 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const PagedCache& c = p.c;
     const int ng = c.ng, nh = kGroup * ng;
-    const PagedWs L = paged_ws(c.B, c.T, ng, p.step_ctas, p.chunk_ctas);
+    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
     const PagedPlanHeader* hdr = reinterpret_cast<const PagedPlanHeader*>(p.ws + L.header);
     const float* part = reinterpret_cast<const float*>(p.ws + L.cpart);
     griddep_wait();
     PagedShare s;
-    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.cprefix);
-    if (!paged_share_begin(s, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.cgroups), prefix, ng,
+    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.prefix);
+    if (!paged_share_begin(s, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.groups), prefix, ng,
                            blockIdx.x + 1, p.chunk_ctas))
         return;
     PagedSeg sg;
     if (!paged_share_next(s, sg, true) || sg.t0 == 0) return;   // the share begins with a pair
-    const PagedParts pp = paged_parts(hdr->chunk, prefix, sg, ng, p.chunk_ctas);
+    const long long W = hdr->chunk.tiles * ng, G = W < (long long)p.chunk_ctas ? W : (long long)p.chunk_ctas;
+    const PagedParts pp = paged_parts(W, G, W * ((long long)blockIdx.x + 1) / G - sg.t0, sg.g.tiles);
     if (pp.cf != (int)blockIdx.x) return;                       // an earlier block folds this pair
     const int row = 32 * blockIdx.y + lane, tok = row >> 3;
     if (4 * (int)blockIdx.y >= sg.g.nrows) return;
@@ -992,6 +1110,8 @@ flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s) {
     if (st == FLINT_OK) st = pc_map(enc, &m[4], bf, p.out, nh, c.T, kGroup, 1);
     if (st != FLINT_OK) return st;
     if (fp8) m[1] = m[2] = m[0];                    // not used
+    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: plan");
     const cudaError_t e = fp8 ? launch_chunk<true>(m, p, s) : launch_chunk<false>(m, p, s);
     if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return FLINT_OK;

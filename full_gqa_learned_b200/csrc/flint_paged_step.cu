@@ -1,5 +1,4 @@
-// Attention of few new tokens per sequence over paged keys and values: the
-// plan of a call and the step kernel.
+// Attention of few new tokens per sequence over paged keys and values.
 //
 // For new row i of sequence b at position p = len[b] + i and query head h of
 // KV head g = h / 8 (FlintAttention.forward on the NeMo AutoModel
@@ -19,9 +18,10 @@
 // * Work is the 64-position (8-bit pages: 128) tiles of all (group, head)
 //   pairs in a row; CTA c takes tiles [W c / G, W (c + 1) / G), whatever
 //   sequences they belong to, so every CTA streams the same number of bytes
-//   for any mix of lengths.  A (group, head) inside one CTA is written at
-//   once; otherwise its CTAs leave partials (m, l, O) and the last to finish
-//   folds them in CTA order, so results do not depend on timing.
+//   for any mix of lengths.  Each CTA works its share out from the lengths
+//   (no planning launch in front).  A (group, head) inside one CTA is written
+//   at once; otherwise its CTAs leave partials (m, l, O), folded in CTA order
+//   by the kernel behind (results do not depend on timing).
 // * A warp takes 16 (32) positions of each tile.  It copies its rows with
 //   16-byte cp.async into a ring of three stages that only itself reads: each
 //   lane fetches the very chunks that its matrix fragments need, so no
@@ -56,149 +56,9 @@ constexpr int kStepWarps = kStepThreads / 32;
 constexpr int kStepStages = 3;
 constexpr int kStepStageBytes = 8192;                    // a warp's K and V rows of one tile
 constexpr int kStepCtasPerSm = 2;
-constexpr int kPlanThreads = 1024;
 
 // Positions of a warp's block and of a tile.
 template <bool FP8> struct StepTile { static constexpr int block = FP8 ? 32 : 16, tile = block * kStepWarps; };
-
-// ---------------------------------------------------------------- plan
-// Exclusive prefix of v over the block; the block's total in *total.
-template <typename I>
-__device__ __forceinline__ I plan_scan(I v, I* sh, I* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    I x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const I y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        I w = sh[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const I y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        sh[lane] = w;
-    }
-    __syncthreads();
-    const I r = x - v + (warp ? sh[warp - 1] : 0);
-    *total = sh[31];
-    __syncthreads();
-    return r;
-}
-
-// Sequence b's new tokens; 0 (and *bad) where its entries are ill-formed.
-__device__ __forceinline__ int plan_new(const PagedAttnParams& p, int b, bool* bad) {
-    const PagedCache& c = p.c;
-    const int a = c.cu[b], z = c.cu[b + 1], len = c.len[b], n = z - a;
-    bool ok = a >= 0 && z >= a && z <= c.T && n <= p.max_new && len >= 0 && len < FLINT_MAX_TOKENS;
-    if (ok && n > 0) {
-        const long long end = (long long)len + n;
-        ok = end <= FLINT_MAX_TOKENS && end <= ((long long)c.max_pages << c.ps_log2);
-    }
-    if (!ok) *bad = true;
-    return ok ? n : 0;
-}
-
-// Groups of one list, from the group offsets of its sequences (first[b],
-// kept in `off`: shared memory up to kPlanSeqs sequences).
-constexpr int kPlanSeqs = 4096;
-__device__ void plan_list(const PagedAttnParams& p, const PagedListSpec& q, PagedGroup* groups, long long* prefix,
-                          int* arrive, PagedList* out, int* off, int* s_bad, int* sh_i, long long* sh_l) {
-    const PagedCache& c = p.c;
-    const int tid = threadIdx.x;
-    // group offsets; past kPlanSeqs sequences the table is a sparse one (every
-    // `every`-th sequence) and the rest is walked
-    const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
-    int n_groups = 0;
-    for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
-        const int b1 = b0 + tid * every;
-        int cnt = 0;
-        bool bad = false;
-        for (int b = b1; b < min(b1 + every, c.B); ++b) {
-            const int n = plan_new(p, b, &bad);
-            if (n >= q.n_min && n <= q.n_max) cnt += (n + q.nt - 1) / q.nt;
-        }
-        if (bad) *s_bad = 1;
-        int tot;
-        const int ex = plan_scan(cnt, sh_i, &tot);
-        if (b1 < c.B) off[b1 / every] = n_groups + ex;
-        n_groups += tot;
-    }
-    __syncthreads();
-    const int n_off = (c.B + every - 1) / every;
-    long long tiles = 0;
-    for (int g0 = 0; g0 < n_groups; g0 += kPlanThreads) {
-        const int g = g0 + tid;
-        PagedGroup r = {};
-        if (g < n_groups) {
-            int lo = 0, hi = n_off - 1;                       // last entry with off <= g
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (off[mid] <= g) lo = mid; else hi = mid - 1;
-            }
-            int at = off[lo], b = lo * every;
-            bool bad = false;
-            for (;; ++b) {                                    // one step where every == 1
-                const int n = plan_new(p, b, &bad);
-                const int k = n >= q.n_min && n <= q.n_max ? (n + q.nt - 1) / q.nt : 0;
-                if (g < at + k || b == c.B - 1) {
-                    r.b = b;
-                    const int row0 = (g - at) * q.nt;
-                    r.nrows = min(q.nt, n - row0);
-                    r.p0 = c.len[b] + row0;
-                    r.row = c.cu[b] + row0;
-                    const int first = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
-                    r.tiles = (r.p0 + r.nrows - (first & ~(q.align - 1)) + q.tile - 1) / q.tile;
-                    break;
-                }
-                at += k;
-            }
-        }
-        long long tot;
-        const long long ex = plan_scan((long long)r.tiles, sh_l, &tot);
-        if (g < n_groups) {
-            groups[g] = r;
-            prefix[g] = tiles + ex;
-            if (arrive)
-                for (int h = 0; h < c.ng; ++h) arrive[(size_t)g * c.ng + h] = 0;
-        }
-        tiles += tot;
-    }
-    if (tid == 0) {
-        prefix[n_groups] = tiles;
-        out->n = n_groups;
-        out->tiles = tiles;
-    }
-    __syncthreads();
-}
-
-// One block: checks the boundaries and lengths, writes the lists of the step
-// and the chunk kernel (chunk_ctas > 0), clears the step kernel's arrival
-// counters and leaves the rotation frequencies.
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p, const PagedListSpec step,
-                                                                  const PagedListSpec chunk) {
-    griddep_launch_dependents();
-    __shared__ int s_bad, s_i[32], s_off[kPlanSeqs];
-    __shared__ long long s_l[32];
-    const int tid = threadIdx.x;
-    const PagedCache& c = p.c;
-    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas);
-    PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
-    double* inv = reinterpret_cast<double*>(p.ws + L.inv);
-    if (tid == 0) s_bad = (c.cu[0] != 0 || c.cu[c.B] > c.T) ? 1 : 0;
-    if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
-    __syncthreads();
-    plan_list(p, step, reinterpret_cast<PagedGroup*>(p.ws + L.sgroups), reinterpret_cast<long long*>(p.ws + L.sprefix),
-              reinterpret_cast<int*>(p.ws + L.arrive), &hdr->step, s_off, &s_bad, s_i, s_l);
-    if (p.chunk_ctas > 0)
-        plan_list(p, chunk, reinterpret_cast<PagedGroup*>(p.ws + L.cgroups),
-                  reinterpret_cast<long long*>(p.ws + L.cprefix), nullptr, &hdr->chunk, s_off, &s_bad, s_i, s_l);
-    if (tid == 0) hdr->status = s_bad ? kStatusInvalid : kStatusOk;
-}
 
 // ---------------------------------------------------------------- step kernel
 __device__ __forceinline__ float st_ex2(float x) {
@@ -263,12 +123,139 @@ struct StepSmem {
     static constexpr uint32_t ml = q + rows * kHD * 2;                                 // [warp][rows] m, then l
     static constexpr uint32_t fin = ml + 2 * kStepWarps * rows * 4;                    // [rows] output scale
     static constexpr uint32_t inv = (fin + rows * 4 + 15) / 16 * 16;                   // rotation frequencies
-    static constexpr uint32_t misc = inv + 64 * 8;
+    static constexpr uint32_t w = inv + 64 * 8;                                        // q_norm weight
+    static constexpr uint32_t sink = w + kHD * 4;                                      // the learned sinks
+    static constexpr uint32_t misc = sink + kHQ * 4;
     static constexpr uint32_t total = misc + 16;
     // a warp's part of a pair, kept in the ring stage it has just read
     static_assert(rows * kHD * 4 <= kStepStageBytes, "a warp's output fits a stage");
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
+
+// A walk over a share of the step's work: the pairs (row group, KV head),
+// sequence by sequence, group by group, head by head.
+struct StepWalk {
+    int b, a, n, len;            // the sequence, its first packed row, new tokens, cached positions
+    int z1, len1;                // the next sequence's end and cached positions, on their way
+    int row0, head, off, left;   // next pair: first row, head, tile it is entered at; tiles left in the share
+};
+struct StepSeg {
+    int b, head, p0, row, nrows, tiles, t0, t1;
+    bool whole, first;
+};
+__device__ __forceinline__ int step_tiles(int window, int p0, int nrows, int tile) {
+    const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
+    return (p0 + nrows - (lo & ~15) + tile - 1) / tile;
+}
+__device__ __forceinline__ void step_enter(const PagedAttnParams& p, StepWalk& w, int b, int a, int z, int len) {
+    const PagedCache& c = p.c;
+    for (;; ++b) {
+        const int n = paged_new(c, p.max_new, a, z, len);
+        w.b = b;
+        w.a = a;
+        w.n = n;
+        w.len = len;
+        const bool more = b + 1 < c.B;
+        w.z1 = more ? __ldg(c.cu + b + 2) : 0;
+        w.len1 = more ? __ldg(c.len + b + 1) : 0;
+        if (n > 0 || !more) return;
+        a = z;
+        z = w.z1;
+        len = w.len1;
+    }
+}
+template <int NT>
+__device__ __forceinline__ bool step_next(const PagedAttnParams& p, StepWalk& w, StepSeg& s, int tile) {
+    if (w.left <= 0) return false;
+    s.b = w.b;
+    s.head = w.head;
+    s.p0 = w.len + w.row0;
+    s.row = w.a + w.row0;
+    s.nrows = min(NT, w.n - w.row0);
+    s.tiles = step_tiles(p.window, s.p0, s.nrows, tile);
+    s.t0 = w.off;
+    s.t1 = min(s.tiles, w.off + w.left);
+    s.whole = s.t0 == 0 && s.t1 == s.tiles;
+    w.left -= s.t1 - s.t0;
+    w.off = 0;
+    if (++w.head == p.c.ng) {
+        w.head = 0;
+        w.row0 += NT;
+        if (w.row0 >= w.n) {
+            w.row0 = 0;
+            if (w.left > 0) step_enter(p, w, w.b + 1, __ldg(p.c.cu + w.b + 1), w.z1, w.len1);
+        }
+    }
+    return true;
+}
+// The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
+// share them; *bad: ill-formed boundaries or lengths.  Every thread of the
+// block (kStepThreads) calls it; false: no share.
+struct StepPlanSmem { long long scan[kStepWarps]; StepWalk walk; int bad; };
+template <int NT>
+__device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas, StepPlanSmem* sm, StepWalk& w, long long* W,
+                          long long* G, bool* bad) {
+    const PagedCache& c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) sm->bad = c.cu[0] != 0 || c.cu[c.B] > c.T;
+    __syncthreads();
+    // a run of sequences a thread
+    const int per = (c.B + kStepThreads - 1) / kStepThreads, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int len = __ldg(c.len + b);
+        const int n = paged_new(c, p.max_new, __ldg(c.cu + b), __ldg(c.cu + b + 1), len);
+        if (n < 0) sm->bad = 1;
+        for (int r = 0; r < n; r += NT) sum += step_tiles(p.window, len + r, min(NT, n - r), tile);
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) sm->scan[warp] = inc;
+    __syncthreads();
+    long long before = inc - sum, total = 0;
+#pragma unroll
+    for (int x = 0; x < kStepWarps; ++x) {
+        if (x < warp) before += sm->scan[x];
+        total += sm->scan[x];
+    }
+    *bad = sm->bad != 0;
+    *W = total * c.ng;
+    *G = *W < (long long)ctas ? *W : (long long)ctas;
+    if (cta >= *G) return false;
+    const long long t = *W * cta / *G, end = *W * (cta + 1) / *G;
+    if (t >= before * c.ng && t < (before + sum) * c.ng) {
+        // the share begins in this thread's run
+        long long in = t - before * c.ng;
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(c.len + b), a = __ldg(c.cu + b), z = __ldg(c.cu + b + 1);
+            const int n = paged_new(c, p.max_new, a, z, len);
+            int r = 0;
+            long long tl = 0;
+            for (; r < n; r += NT) {
+                tl = step_tiles(p.window, len + r, min(NT, n - r), tile);
+                if (in < tl * c.ng) break;
+                in -= tl * c.ng;
+            }
+            if (r < n) {
+                StepWalk v;
+                step_enter(p, v, b, a, z, len);
+                v.row0 = r;
+                v.head = (int)(in / tl);
+                v.off = (int)(in - v.head * tl);
+                v.left = (int)(end - t);
+                sm->walk = v;
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    w = sm->walk;
+    return true;
+}
 
 template <int NT, bool FP8>
 __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kernel(const PagedAttnParams p) {
@@ -282,27 +269,33 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const int j = lane >> 2, i = lane & 3;
     const PagedCache& c = p.c;
     const int ng = c.ng, nh = kGroup * ng;
-    const PagedWs L = paged_ws(c.B, c.T, ng, p.step_ctas, p.chunk_ctas);
-    PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
-    int* arrive = reinterpret_cast<int*>(p.ws + L.arrive);
+    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
     float* s_fin = reinterpret_cast<float*>(smem + S::fin);
+    float* s_w = reinterpret_cast<float*>(smem + S::w);
+    float* s_sink = reinterpret_cast<float*>(smem + S::sink);
     double* s_inv = reinterpret_cast<double*>(smem + S::inv);
-    int* s_last = reinterpret_cast<int*>(smem + S::misc);
 
-    const float mq = warp_max_abs128(p.q_norm_w);        // an input, not the plan's: before the wait
+    griddep_launch_dependents();                         // the combine kernel, which waits for this one
+    const float mq = warp_max_abs128(p.q_norm_w);
     const int eq = prescale_exponent(mq);
     const float C = ldexpf(1.4426950408889634f * 0.08838834764831845f, -eq);   // log2(e) / sqrt(128)
     const float qscale = ldexpf(1.f, eq);
-    griddep_wait();
-
-    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.sprefix);
-    PagedShare share;
-    if (!paged_share_begin(share, hdr->step, reinterpret_cast<const PagedGroup*>(p.ws + L.sgroups), prefix, ng, blockIdx.x,
-                           gridDim.x))
+    s_w[tid] = p.q_norm_w[tid];
+    if (tid < nh) s_sink[tid] = p.sinks[tid];
+    if (p.use_rope && tid < 64) s_inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
+    StepWalk walk;
+    long long W, G;
+    bool bad;
+    if (!step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad)) {
+        if (tid == 0) *reinterpret_cast<int*>(p.ws + L.flags + sizeof(int) * blockIdx.x) = bad ? 1 : 0;
         return;
+    }
+    int* s_bad = reinterpret_cast<int*>(smem + S::misc);
+    if (tid == 0) *s_bad = bad ? 1 : 0;
+    __syncthreads();                                     // the plan's shared memory becomes the ring
 
     // ---- loading.  The stream of tiles runs across pairs: the cursor (f_*)
     // is two tiles ahead of the one being multiplied, in the next pair if need
@@ -312,11 +305,11 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
     const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
     const int slot_mask = (1 << c.ps_log2) - 1;
-    PagedShare f_share = share;
+    StepWalk f_walk = walk;
     int f_left = 0, f_key = 0, f_lo = 0, f_hi = 0, f_head = 0;   // tiles left in its pair; its warp's next key; what is seen
     const int* f_table = nullptr;
     int pg[kSub];                                        // pages of its next tile
-    auto see = [&](const PagedGroup& g, int* lo, int* hi) {
+    auto see = [&](const StepSeg& g, int* lo, int* hi) {
         *lo = p.window > 0 ? max(0, g.p0 - p.window + 1) : 0;
         *hi = g.p0 + g.nrows;
     };
@@ -328,14 +321,15 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
         }
     };
     auto next_pair = [&]() {
-        PagedSeg s;
-        if (!paged_share_next(f_share, s, false)) return;
-        see(s.g, &f_lo, &f_hi);
+        StepSeg s;
+        if (!step_next<NT>(p, f_walk, s, TL::tile)) return;
+        see(s, &f_lo, &f_hi);
         f_left = s.t1 - s.t0;
         f_head = s.head;
         f_key = (f_lo & ~15) + s.t0 * TL::tile + warp * TL::block;
-        f_table = c.table + (size_t)s.g.b * c.max_pages;
+        f_table = c.table + (size_t)s.b * c.max_pages;
         fetch_pages();
+        if (tid < s.nrows) bulk_prefetch_l2(p.q + ((size_t)(s.row + tid) * nh + kGroup * s.head) * kHD, kGroup * kHD * 2);
     };
     const int koff = j * kRowBytes + i * 16, voff = 2 * i * kRowBytes + j * 16;
     auto issue = [&](int stage) {
@@ -345,7 +339,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             for (int u = 0; u < kSub; ++u) {
                 const int key = f_key + 16 * u;
                 const bool live = pg[u] >= 0 && pg[u] < c.num_pages;
-                if (!live && key < f_hi && key + 16 > f_lo && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
+                if (!live && key < f_hi && key + 16 > f_lo) *s_bad = 1;
                 const size_t row = live ? paged_row(c, pg[u], f_head, key & slot_mask) : 0;
                 const uint8_t* kr = kp + row * kRowBytes + koff;
                 const uint8_t* vr = vp + row * kRowBytes + voff;
@@ -385,22 +379,21 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     next_pair();
 #pragma unroll
     for (int s = 0; s < kStepStages - 1; ++s) issue(s);
-    if (p.use_rope && tid < 64) s_inv[tid] = reinterpret_cast<const double*>(p.ws + L.inv)[tid];
 
     int stage = 0;
-    PagedSeg sg;
-    for (bool first = true; paged_share_next(share, sg, first); first = false) {
-        const int head = sg.head, p0 = sg.g.p0, nrows = sg.g.nrows;
+    StepSeg sg;
+    for (bool first = true; step_next<NT>(p, walk, sg, TL::tile); first = false) {
+        const int head = sg.head, p0 = sg.p0, nrows = sg.nrows;
         int lo, hi;
-        see(sg.g, &lo, &hi);
-        __syncthreads();                                 // s_inv; the last pair's q~ is read
+        see(sg, &lo, &hi);
+        __syncthreads();                                 // the last pair's q~ and parts are read
 
         // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
         if (warp < 2 * NT) {
             const int nt = warp >> 1, sub = lane & 7, hh = 4 * (warp & 1) + (lane >> 3);
             const bool have = nt < nrows;
             const int pos = p0 + (have ? nt : 0);
-            const __nv_bfloat16* src = p.q + ((size_t)(sg.g.row + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
+            const __nv_bfloat16* src = p.q + ((size_t)(sg.row + (have ? nt : 0)) * nh + kGroup * head + hh) * kHD;
             const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * sub);
             const uint4 b = *reinterpret_cast<const uint4*>(src + 64 + 8 * sub);
             float x0[8], x1[8], ss = 0.f;
@@ -417,8 +410,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             const float rn = qscale * rsqrtf(ss * (1.f / kHD) + p.eps);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                x0[e] *= rn * p.q_norm_w[8 * sub + e];
-                x1[e] *= rn * p.q_norm_w[64 + 8 * sub + e];
+                x0[e] *= rn * s_w[8 * sub + e];
+                x1[e] *= rn * s_w[64 + 8 * sub + e];
             }
             if (p.use_rope) {
                 float c0, s0, c1, s1;
@@ -683,8 +676,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 }
             }
         const int rows = kGroup * nrows;
-        const size_t out_row = (size_t)sg.g.row;
-        float* dst = part + (2 * (size_t)blockIdx.x + (sg.first ? 0 : 1)) * kStepPart;   // where the pair is held in part
+        const size_t out_row = (size_t)sg.row;
+        float* dst = part + (2 * (size_t)blockIdx.x + (first ? 0 : 1)) * kStepPart;   // where the pair is held in part
         if (tid < rows) {
             float M = s_m[tid], l4 = 0.f;
 #pragma unroll
@@ -697,7 +690,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             if (sg.whole) {
                 const int h = kGroup * head + (tid & 7);
                 float v;
-                paged_finish(M, l4, p.sinks[h], &s_fin[tid], &v);
+                paged_finish(M, l4, s_sink[h], &s_fin[tid], &v);
                 if (p.lse) p.lse[(size_t)h * c.T + out_row + (tid >> 3)] = v;
             } else {
                 dst[tid] = M;
@@ -727,88 +720,76 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 *reinterpret_cast<float4*>(dst + 2 * kPagedStepRows + r * kHD + 4 * lane) = o;
             }
         }
-        if (sg.whole) continue;                          // the next pair begins with a barrier
-
-        // ---- the last of the pair's CTAs to finish folds their parts in CTA order
-        const PagedParts pp = paged_parts(hdr->step, prefix, sg, ng, gridDim.x);
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) *s_last = atomicAdd(arrive + (size_t)sg.gi * ng + head, 1) == pp.cl - pp.cf;
-        __syncthreads();
-        if (*s_last) {
-            __threadfence();
-            // warp w adds CTAs cf + w, + 4, .. (every row: independent loads),
-            // the warps meet in the buffers above
-            float M[S::rows / 8], Ls[S::rows / 8];        // lane: row lane / 4 (+ 8), of CTAs lane % 4, + 4, ..
-#pragma unroll
-            for (int x = 0; x < S::rows / 8; ++x) M[x] = -INFINITY;
-            for (int y = pp.cf + i; y <= pp.cl; y += 4)
-#pragma unroll
-                for (int x = 0; x < S::rows / 8; ++x)
-                    if (j + 8 * x < rows) M[x] = fmaxf(M[x], __ldcg(part + pp.slot(y) * kStepPart + j + 8 * x));
-#pragma unroll
-            for (int x = 0; x < S::rows / 8; ++x) {
-                M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], 1));
-                M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], 2));
-                Ls[x] = 0.f;
-            }
-            float4 o[S::rows];
-#pragma unroll
-            for (int r = 0; r < S::rows; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int y = pp.cf + warp; y <= pp.cl; y += kStepWarps) {
-                const float* b = part + pp.slot(y) * kStepPart;
-                float a[S::rows / 8];
-#pragma unroll
-                for (int x = 0; x < S::rows / 8; ++x) {
-                    a[x] = 0.f;
-                    if (j + 8 * x < rows) {
-                        const float ms = __ldcg(b + j + 8 * x), ls = __ldcg(b + kPagedStepRows + j + 8 * x);
-                        a[x] = ms > -INFINITY ? exp2f(ms - M[x]) : 0.f;
-                        Ls[x] += ls * a[x];
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < S::rows; ++r) {
-                    if (r >= rows) break;
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(b + 2 * kPagedStepRows + r * kHD) + lane);
-                    const float ar = __shfl_sync(0xffffffffu, a[r >> 3], 4 * (r & 7));
-                    o[r].x += v.x * ar;
-                    o[r].y += v.y * ar;
-                    o[r].z += v.z * ar;
-                    o[r].w += v.w * ar;
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < S::rows; ++r) *reinterpret_cast<float4*>(buf + r * kHD + 4 * lane) = o[r];
-            if (i == 0)
-#pragma unroll
-                for (int x = 0; x < S::rows / 8; ++x) {
-                    s_m[warp * S::rows + j + 8 * x] = M[x];
-                    s_l[warp * S::rows + j + 8 * x] = Ls[x];
-                }
-            __syncthreads();
-            for (int r = warp; r < rows; r += kStepWarps) {
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-                float l4 = 0.f;
-#pragma unroll
-                for (int w = 0; w < kStepWarps; ++w) {
-                    const float4 v = *reinterpret_cast<const float4*>(bufs + w * kBufStep + r * kHD + 4 * lane);
-                    t.x += v.x;
-                    t.y += v.y;
-                    t.z += v.z;
-                    t.w += v.w;
-                    l4 += s_l[w * S::rows + r];
-                }
-                const int h = kGroup * head + (r & 7);
-                float sc, v;
-                paged_finish(s_m[r], l4, p.sinks[h], &sc, &v);
-                *reinterpret_cast<uint2*>(p.out + ((out_row + (r >> 3)) * nh + h) * kHD + 4 * lane) =
-                    make_uint2(pack2_bf16(t.x * sc, t.y * sc), pack2_bf16(t.z * sc, t.w * sc));
-                if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + out_row + (r >> 3)] = v;
-            }
-        }
     }
     cp_wait<0>();
+    __syncthreads();
+    if (tid == 0) *reinterpret_cast<int*>(p.ws + L.flags + sizeof(int) * blockIdx.x) = *s_bad;
+}
+
+// Folds the parts of the pairs that several CTAs hold, in CTA order; block x:
+// the pair that CTA x + 1's share begins inside of, if x + 1 is the first CTA
+// to do so.  A warp takes a row (block y: rows 4 y .. + 3), a lane four
+// channels.  Block (0, 0) also collects the CTAs' flags into the status word.
+template <int NT, bool FP8>
+__global__ void __launch_bounds__(kStepThreads, 4) paged_fold_kernel(const PagedAttnParams p) {
+    __shared__ StepPlanSmem sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const PagedCache& c = p.c;
+    const int nh = kGroup * c.ng;
+    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
+    const float* part = reinterpret_cast<const float*>(p.ws + L.spart);
+    StepWalk walk;
+    long long W, G;
+    bool bad;
+    const bool work = step_plan<NT>(p, StepTile<FP8>::tile, blockIdx.x + 1, p.step_ctas, &sm, walk, &W, &G, &bad);
+    griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        bool any = bad;
+        for (int x = tid; x < p.step_ctas; x += kStepThreads) any = any || reinterpret_cast<const int*>(p.ws + L.flags)[x] != 0;
+        if (__syncthreads_or(any) && tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = kStatusInvalid;
+        else if (tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = kStatusOk;
+    }
+    StepSeg sg;
+    if (!work || !step_next<NT>(p, walk, sg, StepTile<FP8>::tile) || sg.t0 == 0) return;   // the share begins with a pair
+    const PagedParts pp = paged_parts(W, G, W * ((long long)blockIdx.x + 1) / G - sg.t0, sg.tiles);
+    if (pp.cf != (int)blockIdx.x) return;                // an earlier block folds this pair
+    const int r = kStepWarps * blockIdx.y + warp;        // the warp's row
+    if (r < kGroup * sg.nrows) {
+        float M = -INFINITY;
+        for (int x = pp.cf + lane; x <= pp.cl; x += 32) M = fmaxf(M, part[pp.slot(x) * kStepPart + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAhead = 12;                       // parts on their way at once
+        for (int x0 = pp.cf; x0 <= pp.cl; x0 += kAhead) {
+            float mx[kAhead], lx[kAhead];
+            float4 v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float* b = part + pp.slot(min(x0 + k, pp.cl)) * kStepPart;
+                mx[k] = __ldcg(b + r);
+                lx[k] = __ldcg(b + kPagedStepRows + r);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(b + 2 * kPagedStepRows + r * kHD) + lane);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float a = mx[k] > -INFINITY && x0 + k <= pp.cl ? exp2f(mx[k] - M) : 0.f;
+                l += lx[k] * a;
+                o.x += v[k].x * a;
+                o.y += v[k].y * a;
+                o.z += v[k].z * a;
+                o.w += v[k].w * a;
+            }
+        }
+        const int h = kGroup * sg.head + (r & 7);
+        const size_t row = (size_t)sg.row + (r >> 3);
+        float sc, lse;
+        paged_finish(M, l, p.sinks[h], &sc, &lse);
+        *reinterpret_cast<uint2*>(p.out + (row * nh + h) * kHD + 4 * lane) =
+            make_uint2(pack2_bf16(o.x * sc, o.y * sc), pack2_bf16(o.z * sc, o.w * sc));
+        if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + row] = lse;
+    }
 }
 
 // ============================================================================ host
@@ -825,49 +806,47 @@ cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
+    paged_step_kernel<NT, FP8><<<p.step_ctas, kStepThreads, StepSmem<NT>::total, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.step_ctas);
+    cfg.gridDim = dim3(p.step_ctas > 1 ? p.step_ctas - 1 : 1, kGroup * NT / kStepWarps);
     cfg.blockDim = dim3(kStepThreads);
-    cfg.dynamicSmemBytes = StepSmem<NT>::total;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_step_kernel<NT, FP8>, p);
+    return cudaLaunchKernelEx(&cfg, paged_fold_kernel<NT, FP8>, p);
 }
 
 // The workspace does not depend on the device: room for a full B200's CTAs.
 constexpr int kPagedMaxSms = 148;
 
 // Calls whose sequences all have at most this many new tokens run the step
-// kernel alone.
+// kernel, others the chunk kernel.
 constexpr int kStepMaxNew = 8;
 
 }  // namespace
 
 size_t paged_attn_workspace(int B, int T, int max_new, int ng) {
-    return paged_ws(B, T, ng, kPagedMaxSms * kStepCtasPerSm, max_new > kStepMaxNew ? kPagedMaxSms : 0).total;
+    (void)ng;
+    return paged_ws(B, T, kPagedMaxSms * kStepCtasPerSm, max_new > kStepMaxNew ? kPagedMaxSms : 0).total;
 }
 
 flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, cudaStream_t s) {
+    (void)c;
     PagedAttnParams p = in;
     if (sms > kPagedMaxSms) sms = kPagedMaxSms;
     p.step_ctas = sms * kStepCtasPerSm;
     p.chunk_ctas = p.max_new > kStepMaxNew ? sms : 0;
+    if (p.chunk_ctas) return launch_paged_chunk(p, s);
     const bool fp8 = p.k_scales != nullptr;
-    const int nt = p.max_new > 1 ? 2 : 1;
-    // with the chunk kernel in the call, it takes every sequence
-    const PagedListSpec step = {1, p.chunk_ctas ? 0 : 0x7fffffff, nt, fp8 ? StepTile<true>::tile : StepTile<false>::tile, 16};
-    const PagedListSpec chunk = {1, 0x7fffffff, kChunkTok, kKeyChunk, 1 << c.ps_log2};
-    paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, step, chunk);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && !p.chunk_ctas)
-        e = nt == 1 ? (fp8 ? launch_step<1, true>(p, s) : launch_step<1, false>(p, s))
-                    : (fp8 ? launch_step<2, true>(p, s) : launch_step<2, false>(p, s));
+    const cudaError_t e = p.max_new > 1 ? (fp8 ? launch_step<2, true>(p, s) : launch_step<2, false>(p, s))
+                                        : (fp8 ? launch_step<1, true>(p, s) : launch_step<1, false>(p, s));
     if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
-    return p.chunk_ctas ? launch_paged_chunk(p, s) : FLINT_OK;
+    return FLINT_OK;
 }
 
 }  // namespace flint
