@@ -22,25 +22,34 @@
 //   (no planning launch in front).  A (group, head) inside one CTA is written
 //   at once; otherwise its CTAs leave partials (m, l, O), folded in CTA order
 //   by the kernel behind (results do not depend on timing).
-// * A warp takes 16 (32) positions of each tile.  It copies its rows with
-//   16-byte cp.async into a ring of three stages that only itself reads: each
-//   lane fetches the very chunks that its matrix fragments need, so no
-//   barrier and no bank conflict stands between memory and the MMA.
+// * A producer warp streams the tiles by TMA (three stages of 32 KiB, two CTAs
+//   an SM), across the pairs of its share: interior tiles in boxes as tall as
+//   a page and tile allow, a pair's edges in boxes of 16 slots, so that next
+//   to nothing outside the window is read.  (Sixteen-byte cp.async copies by
+//   the consuming lanes, with the products left out, took as long as with
+//   them: 94 us for 450 MB, 4.8 TB/s.)  It also brings the next pair's
+//   queries to L2 and copies the scales of 8-bit pages.
+// * Four consumer warps take 16 (32) positions of each tile each; nothing but
+//   a pair's end joins them.  Fragments come from the 128-byte-swizzled tiles
+//   without bank conflicts:
 //     K (A operand, 16 keys x 16 channels): lane (j, i) = (lane / 4,
-//     lane % 4) holds 16-byte chunks 4 c + i of rows j and j + 8; the channel
-//     order that gives is used for q~ (B operand) too.
+//     lane % 4) reads 16-byte chunks 2 i and 2 i + 1 of each 128 bytes of
+//     rows j and j + 8; the channel order that gives is used for q~ (B
+//     operand) too.
 //     V (A operand of O^T += V^T P^T, 16 channels x 16 keys): lane (j, i)
-//     holds chunk j of rows 2 i, 2 i + 1, 2 i + 8, 2 i + 9 and interleaves
+//     reads chunk j of rows 2 i, 2 i + 1, 2 i + 8, 2 i + 9 and interleaves
 //     pairs of rows; rows of the product are the channels of its chunks.
 // * S^T = K Q^T has the head pairs (2 i, 2 i + 1) of keys j and j + 8 in lane
 //   (j, i): the softmax needs no exchange as long as the running max stands.
 //   It is raised only when a score passes it by 2^8 (a vote a block).
 //   movmatrix turns P^T into the next B operand.
-// * q~ is split into FP16 high and low parts (both multiplied), and so is P
-//   for BF16 values: neither rounding shows beside the output's.  8-bit
+// * q~ is FP16, as in the forward; P for BF16 values is split into high and
+//   low parts (both multiplied), so its rounding does not show.  8-bit
 //   values: the codes are exact in FP16 and the scale 2^e joins the exponent,
 //   p' = 2^(z + e - m), with m the maximum of z + e, while l sums
 //   p' 2^-e; P' carries FP16's 11 bits where its product matters.
+// Every wait is bounded (FLINT_ERR_TIMEOUT in the status word).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "flint_host.cuh"
@@ -51,14 +60,18 @@ namespace flint {
 
 flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s);
 
-constexpr int kStepThreads = 128;
-constexpr int kStepWarps = kStepThreads / 32;
-constexpr int kStepStages = 3;
-constexpr int kStepStageBytes = 8192;                    // a warp's K and V rows of one tile
+constexpr int kStepWarps = 4;                            // consumer warps
+constexpr int kStepThreads = 32 * kStepWarps + 32;       // and the producer
+constexpr int kFoldThreads = 128;
+constexpr uint32_t kStepStages = 3;
+constexpr uint32_t kStepHalf = 16384;                    // a tile's keys, or values
+constexpr uint32_t kStepStage = 2 * kStepHalf;
 constexpr int kStepCtasPerSm = 2;
 
-// Positions of a warp's block and of a tile.
-template <bool FP8> struct StepTile { static constexpr int block = FP8 ? 32 : 16, tile = block * kStepWarps; };
+// Positions of a warp's block and of a tile; 16-position pieces of a tile.
+template <bool FP8> struct StepTile {
+    static constexpr int block = FP8 ? 32 : 16, tile = block * kStepWarps, pieces = tile / 16;
+};
 
 // ---------------------------------------------------------------- step kernel
 __device__ __forceinline__ float st_ex2(float x) {
@@ -66,17 +79,9 @@ __device__ __forceinline__ float st_ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 16 bytes global -> shared; zeros where `on` is false (nothing is read then)
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
-    const int n = on ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 r;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
     return r;
 }
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -117,20 +122,22 @@ __device__ __forceinline__ uint32_t reg4(const uint4& v, int i) { return i == 0 
 template <int NT>
 struct StepSmem {
     static constexpr int rows = 8 * NT;
-    static constexpr uint32_t ring = 0;
-    static constexpr uint32_t scales = kStepWarps * kStepStages * kStepStageBytes;     // 64 bytes a stage and warp
-    static constexpr uint32_t q = scales + kStepWarps * kStepStages * 64;              // q~ in FP16
+    static constexpr uint32_t ring = 0;                                                // K, V of a tile; stages
+    static constexpr uint32_t scales = kStepStages * kStepStage;                       // 8 pieces x (K, V) x 16 bytes a stage
+    static constexpr uint32_t q = scales + kStepStages * 256;                          // q~ in FP16
     static constexpr uint32_t ml = q + rows * kHD * 2;                                 // [warp][rows] m, then l
     static constexpr uint32_t fin = ml + 2 * kStepWarps * rows * 4;                    // [rows] output scale
     static constexpr uint32_t inv = (fin + rows * 4 + 15) / 16 * 16;                   // rotation frequencies
     static constexpr uint32_t w = inv + 64 * 8;                                        // q_norm weight
     static constexpr uint32_t sink = w + kHD * 4;                                      // the learned sinks
-    static constexpr uint32_t misc = sink + kHQ * 4;
-    static constexpr uint32_t total = misc + 16;
-    // a warp's part of a pair, kept in the ring stage it has just read
-    static_assert(rows * kHD * 4 <= kStepStageBytes, "a warp's output fits a stage");
+    static constexpr uint32_t bar = sink + kHQ * 4;                                    // full, empty, consumers
+    static constexpr uint32_t misc = bar + 8 * 8;                                      // abort flag, CTA status
+    static constexpr uint32_t total = misc + 16 + 1024;                                // and alignment slack
+    // the warps' parts of a pair meet in the stage read last
+    static_assert(kStepWarps * rows * kHD * 4 <= kStepStage, "the warps' outputs fit a stage");
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
+enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6 };
 
 // A walk over a share of the step's work: the pairs (row group, KV head),
 // sequence by sequence, group by group, head by head.
@@ -143,9 +150,13 @@ struct StepSeg {
     int b, head, p0, row, nrows, tiles, t0, t1;
     bool whole, first;
 };
-__device__ __forceinline__ int step_tiles(int window, int p0, int nrows, int tile) {
-    const int lo = window > 0 ? max(0, p0 - window + 1) : 0;
-    return (p0 + nrows - (lo & ~15) + tile - 1) / tile;
+// Tiles start at a multiple of the box: min(page, tile).
+__device__ __forceinline__ int step_base(const PagedAttnParams& p, int lo, int tile) {
+    return lo & ~(min(1 << p.c.ps_log2, tile) - 1);
+}
+__device__ __forceinline__ int step_tiles(const PagedAttnParams& p, int p0, int nrows, int tile) {
+    const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+    return (p0 + nrows - step_base(p, lo, tile) + tile - 1) / tile;
 }
 __device__ __forceinline__ void step_enter(const PagedAttnParams& p, StepWalk& w, int b, int a, int z, int len) {
     const PagedCache& c = p.c;
@@ -172,7 +183,7 @@ __device__ __forceinline__ bool step_next(const PagedAttnParams& p, StepWalk& w,
     s.p0 = w.len + w.row0;
     s.row = w.a + w.row0;
     s.nrows = min(NT, w.n - w.row0);
-    s.tiles = step_tiles(p.window, s.p0, s.nrows, tile);
+    s.tiles = step_tiles(p, s.p0, s.nrows, tile);
     s.t0 = w.off;
     s.t1 = min(s.tiles, w.off + w.left);
     s.whole = s.t0 == 0 && s.t1 == s.tiles;
@@ -190,9 +201,9 @@ __device__ __forceinline__ bool step_next(const PagedAttnParams& p, StepWalk& w,
 }
 // The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
 // share them; *bad: ill-formed boundaries or lengths.  Every thread of the
-// block (kStepThreads) calls it; false: no share.
-struct StepPlanSmem { long long scan[kStepWarps]; StepWalk walk; int bad; };
-template <int NT>
+// block calls it; false: no share.
+struct StepPlanSmem { long long scan[8]; StepWalk walk; int bad; };
+template <int NT, int THREADS>
 __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas, StepPlanSmem* sm, StepWalk& w, long long* W,
                           long long* G, bool* bad) {
     const PagedCache& c = p.c;
@@ -200,13 +211,13 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     if (tid == 0) sm->bad = c.cu[0] != 0 || c.cu[c.B] > c.T;
     __syncthreads();
     // a run of sequences a thread
-    const int per = (c.B + kStepThreads - 1) / kStepThreads, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+    const int per = (c.B + THREADS - 1) / THREADS, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
         const int len = __ldg(c.len + b);
         const int n = paged_new(c, p.max_new, __ldg(c.cu + b), __ldg(c.cu + b + 1), len);
         if (n < 0) sm->bad = 1;
-        for (int r = 0; r < n; r += NT) sum += step_tiles(p.window, len + r, min(NT, n - r), tile);
+        for (int r = 0; r < n; r += NT) sum += step_tiles(p, len + r, min(NT, n - r), tile);
     }
     long long inc = sum;
 #pragma unroll
@@ -218,7 +229,7 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     __syncthreads();
     long long before = inc - sum, total = 0;
 #pragma unroll
-    for (int x = 0; x < kStepWarps; ++x) {
+    for (int x = 0; x < THREADS / 32; ++x) {
         if (x < warp) before += sm->scan[x];
         total += sm->scan[x];
     }
@@ -236,7 +247,7 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
             int r = 0;
             long long tl = 0;
             for (; r < n; r += NT) {
-                tl = step_tiles(p.window, len + r, min(NT, n - r), tile);
+                tl = step_tiles(p, len + r, min(NT, n - r), tile);
                 if (in < tl * c.ng) break;
                 in -= tl * c.ng;
             }
@@ -257,13 +268,17 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     return true;
 }
 
+// Maps of the pools: k, v in boxes of min(page, tile) slots; k16, v16 of 16.
+struct StepMaps { CUtensorMap k, v, k16, v16; };
+
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm)
+paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p) {
     using S = StepSmem<NT>;
     using TL = StepTile<FP8>;
     constexpr int kSub = FP8 ? 2 : 1;                    // 16-position parts of a warp's block
-    constexpr int kRowBytes = FP8 ? kHD : 2 * kHD;
-    extern __shared__ __align__(1024) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int j = lane >> 2, i = lane & 3;
@@ -271,122 +286,158 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
     const int ng = c.ng, nh = kGroup * ng;
     const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
+    int* flag = reinterpret_cast<int*>(p.ws + L.flags) + blockIdx.x;
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
     float* s_fin = reinterpret_cast<float*>(smem + S::fin);
     float* s_w = reinterpret_cast<float*>(smem + S::w);
     float* s_sink = reinterpret_cast<float*>(smem + S::sink);
     double* s_inv = reinterpret_cast<double*>(smem + S::inv);
+    volatile int* abort_flag = reinterpret_cast<int*>(smem + S::misc);
+    int* s_status = reinterpret_cast<int*>(smem + S::misc) + 1;
+    auto bar = [&](uint32_t x) { return sb + S::bar + 8 * x; };
 
-    griddep_launch_dependents();                         // the combine kernel, which waits for this one
+    griddep_launch_dependents();                         // the fold kernel, which waits for this one
     const float mq = warp_max_abs128(p.q_norm_w);
     const int eq = prescale_exponent(mq);
     const float C = ldexpf(1.4426950408889634f * 0.08838834764831845f, -eq);   // log2(e) / sqrt(128)
     const float qscale = ldexpf(1.f, eq);
-    s_w[tid] = p.q_norm_w[tid];
+    if (tid < kHD) s_w[tid] = p.q_norm_w[tid];
     if (tid < nh) s_sink[tid] = p.sinks[tid];
     if (p.use_rope && tid < 64) s_inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     StepWalk walk;
     long long W, G;
     bool bad;
-    if (!step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad)) {
-        if (tid == 0) *reinterpret_cast<int*>(p.ws + L.flags + sizeof(int) * blockIdx.x) = bad ? 1 : 0;
+    if (!step_plan<NT, kStepThreads>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad)) {
+        if (tid == 0) *flag = bad ? kStatusInvalid : kStatusOk;
         return;
     }
-    int* s_bad = reinterpret_cast<int*>(smem + S::misc);
-    if (tid == 0) *s_bad = bad ? 1 : 0;
+    if (tid == 0) {
+        for (uint32_t x = 0; x < kStepStages; ++x) {
+            mbar_init(bar(ST_FULL + x), 1);
+            mbar_init(bar(ST_EMPTY + x), kStepWarps);
+        }
+        mbar_init(bar(ST_CONS), 32 * kStepWarps);
+        *abort_flag = 0;
+        *s_status = bad ? kStatusInvalid : kStatusOk;
+        fence_mbar_init();
+    }
     __syncthreads();                                     // the plan's shared memory becomes the ring
-
-    // ---- loading.  The stream of tiles runs across pairs: the cursor (f_*)
-    // is two tiles ahead of the one being multiplied, in the next pair if need
-    // be, so that a pair's end does not drain the ring.
-    const uint32_t ring = sb + S::ring + warp * (kStepStages * kStepStageBytes) + lane * 16;
-    const uint32_t srow = sb + S::scales + warp * (kStepStages * 64);
-    const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
-    const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
-    const int slot_mask = (1 << c.ps_log2) - 1;
-    StepWalk f_walk = walk;
-    int f_left = 0, f_key = 0, f_lo = 0, f_hi = 0, f_head = 0;   // tiles left in its pair; its warp's next key; what is seen
-    const int* f_table = nullptr;
-    int pg[kSub];                                        // pages of its next tile
     auto see = [&](const StepSeg& g, int* lo, int* hi) {
         *lo = p.window > 0 ? max(0, g.p0 - p.window + 1) : 0;
         *hi = g.p0 + g.nrows;
     };
-    auto fetch_pages = [&]() {
-#pragma unroll
-        for (int u = 0; u < kSub; ++u) {
-            const int key = f_key + 16 * u;
-            pg[u] = key < f_hi && key + 16 > f_lo ? __ldg(f_table + (key >> c.ps_log2)) : -1;
-        }
-    };
-    auto next_pair = [&]() {
-        StepSeg s;
-        if (!step_next<NT>(p, f_walk, s, TL::tile)) return;
-        see(s, &f_lo, &f_hi);
-        f_left = s.t1 - s.t0;
-        f_head = s.head;
-        f_key = (f_lo & ~15) + s.t0 * TL::tile + warp * TL::block;
-        f_table = c.table + (size_t)s.b * c.max_pages;
-        fetch_pages();
-        if (tid < s.nrows) bulk_prefetch_l2(p.q + ((size_t)(s.row + tid) * nh + kGroup * s.head) * kHD, kGroup * kHD * 2);
-    };
-    const int koff = j * kRowBytes + i * 16, voff = 2 * i * kRowBytes + j * 16;
-    auto issue = [&](int stage) {
-        if (f_left > 0) {
-            const uint32_t dst = ring + stage * kStepStageBytes;
-#pragma unroll
-            for (int u = 0; u < kSub; ++u) {
-                const int key = f_key + 16 * u;
-                const bool live = pg[u] >= 0 && pg[u] < c.num_pages;
-                if (!live && key < f_hi && key + 16 > f_lo) *s_bad = 1;
-                const size_t row = live ? paged_row(c, pg[u], f_head, key & slot_mask) : 0;
-                const uint8_t* kr = kp + row * kRowBytes + koff;
-                const uint8_t* vr = vp + row * kRowBytes + voff;
-                if (live && key >= f_lo && key + 16 <= f_hi) {
-#pragma unroll
-                    for (int x = 0; x < (FP8 ? 4 : 8); ++x) {
-                        if constexpr (FP8) {
-                            cp16(dst + u * 4096 + x * 512, kr + (x >> 1) * 8 * kRowBytes + (x & 1) * 64, true);
-                            cp16(dst + u * 4096 + 2048 + x * 512, vr + ((x & 1) + (x >> 1) * 8) * kRowBytes, true);
-                        } else {
-                            cp16(dst + x * 512, kr + (x >> 2) * 8 * kRowBytes + (x & 3) * 64, true);
-                            cp16(dst + 4096 + x * 512, vr + ((x & 1) + ((x >> 1) & 1) * 8) * kRowBytes + (x >> 2) * 128, true);
-                        }
-                    }
-                } else {
-                    // rows outside [lo, hi) are not read: their slots may hold anything
-                    auto on = [&](int r) { return live && key + r >= f_lo && key + r < f_hi; };
-#pragma unroll
-                    for (int x = 0; x < (FP8 ? 4 : 8); ++x) {
-                        const int kx = FP8 ? (x >> 1) * 8 : (x >> 2) * 8;
-                        const int vx = (x & 1) + ((x >> 1) & 1) * 8;
-                        const bool k_on = on(j + kx), v_on = on(2 * i + vx);
-                        const uint8_t* ks = kr + kx * kRowBytes + (FP8 ? (x & 1) : (x & 3)) * 64;
-                        const uint8_t* vs = vr + vx * kRowBytes + (FP8 ? 0 : (x >> 2) * 128);
-                        cp16(dst + (FP8 ? u * 4096 : 0) + x * 512, k_on ? ks : kp, k_on);
-                        cp16(dst + (FP8 ? u * 4096 + 2048 : 4096) + x * 512, v_on ? vs : vp, v_on);
-                    }
-                }
-                if (FP8 && lane < 2) cp16(srow + stage * 64 + u * 32 + lane * 16, (lane ? p.v_scales : p.k_scales) + row, live);
-            }
-            f_key += TL::tile;
-            if (--f_left > 0) fetch_pages();
-            else next_pair();
-        }
-        cp_commit();
-    };
-    next_pair();
-#pragma unroll
-    for (int s = 0; s < kStepStages - 1; ++s) issue(s);
 
-    int stage = 0;
+    if (warp == kStepWarps) {
+        // ============================================================ producer (the whole warp)
+        // Lane l < pieces holds piece l (16 positions) of a tile: its page, and
+        // for 8-bit pages its scales, both fetched ahead.
+        struct Tile { int key, lo, hi, head, page; bool any; };
+        const int box = min(1 << c.ps_log2, TL::tile), slot_mask = (1 << c.ps_log2) - 1;
+        constexpr uint32_t kPiece = FP8 ? 2048 : 4096;   // bytes of a piece's keys, or values
+        int left = 0, key = 0, lo = 0, hi = 0, head = 0;
+        const int* table = nullptr;
+        auto next_tile = [&]() -> Tile {
+            Tile t = {};
+            if (left == 0) {
+                StepSeg sg;
+                if (!step_next<NT>(p, walk, sg, TL::tile)) return t;
+                see(sg, &lo, &hi);
+                left = sg.t1 - sg.t0;
+                head = sg.head;
+                key = step_base(p, lo, TL::tile) + sg.t0 * TL::tile;
+                table = c.table + (size_t)sg.b * c.max_pages;
+                if (lane < sg.nrows) bulk_prefetch_l2(p.q + ((size_t)(sg.row + lane) * nh + kGroup * head) * kHD, kGroup * kHD * 2);
+            }
+            t.any = true;
+            t.key = key;
+            t.lo = lo;
+            t.hi = hi;
+            t.head = head;
+            const int k = key + 16 * lane;
+            t.page = lane < TL::pieces && k < hi && k + 16 > lo ? __ldg(table + (k >> c.ps_log2)) : -2;
+            key += TL::tile;
+            --left;
+            return t;
+        };
+        auto row_of = [&](const Tile& t) -> long long {   // pool row of the lane's piece, -1 where it has none
+            if (t.page < 0 || t.page >= c.num_pages) return -1;
+            return (long long)paged_row(c, t.page, t.head, (t.key + 16 * lane) & slot_mask);
+        };
+        uint4 ks = {}, vs = {};
+        auto load_scales = [&](const Tile& t) {
+            const long long r = t.any ? row_of(t) : -1;
+            if (FP8 && r >= 0) {
+                ks = __ldg(reinterpret_cast<const uint4*>(p.k_scales + r));
+                vs = __ldg(reinterpret_cast<const uint4*>(p.v_scales + r));
+            }
+        };
+        Tile cur = next_tile(), nxt = next_tile();
+        load_scales(cur);
+        uint32_t st = 0, ph = 0, n = 0;
+        while (cur.any) {
+            const uint4 k0 = ks, v0 = vs;
+            load_scales(nxt);
+            const Tile after = next_tile();
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(ST_EMPTY + st), ph ^ 1, abort_flag, s_status))) break;
+            const bool live = row_of(cur) >= 0;
+            if (!live && cur.page != -2) *s_status = kStatusInvalid;
+            if (FP8 && live) {
+                uint4* d = reinterpret_cast<uint4*>(smem + S::scales + st * 256) + 2 * lane;
+                d[0] = k0;
+                d[1] = v0;
+            }
+            const uint32_t bytes = 2 * kPiece * __popc(__ballot_sync(0xffffffffu, live));
+            __syncwarp();
+            if (lane == 0) mbar_expect_tx(bar(ST_FULL + st), bytes);
+            __syncwarp();
+            const uint32_t dst = sb + S::ring + st * kStepStage + lane * 2048;
+            const int slot = (cur.key + 16 * lane) & slot_mask, z = cur.page * ng + cur.head;
+            const bool inside = cur.key >= cur.lo && cur.key + TL::tile <= cur.hi;   // every row of the tile is seen
+            if (inside ? live && (16 * lane & (box - 1)) == 0 : live) {
+                const CUtensorMap* mk = inside ? &maps.k : &maps.k16;
+                const CUtensorMap* mv = inside ? &maps.v : &maps.v16;
+                if constexpr (FP8) {
+                    tma_load_3d(dst, mk, bar(ST_FULL + st), 0, slot, z);
+                    tma_load_3d(dst + kStepHalf, mv, bar(ST_FULL + st), 0, slot, z);
+                } else {
+                    // the channel halves of a tile are 8 KiB apart
+                    tma_load_3d(dst, mk, bar(ST_FULL + st), 0, slot, z);
+                    tma_load_3d(dst + kStepHalf / 2, mk, bar(ST_FULL + st), 64, slot, z);
+                    tma_load_3d(dst + kStepHalf, mv, bar(ST_FULL + st), 0, slot, z);
+                    tma_load_3d(dst + kStepHalf + kStepHalf / 2, mv, bar(ST_FULL + st), 64, slot, z);
+                }
+            }
+            ++n;
+            if (++st == kStepStages) { st = 0; ph ^= 1; }
+            cur = nxt;
+            nxt = after;
+        }
+        // every armed load has landed before shared memory is released
+        volatile int never = 0;
+        for (uint32_t x = 0; x < kStepStages; ++x) {
+            const uint32_t nl = (n + kStepStages - 1 - x) / kStepStages;     // loads number x, x + 3, ..
+            if (nl) mbar_wait(bar(ST_FULL + x), (nl - 1) & 1, &never, nullptr, 100ull * 1000ull * 1000ull);
+        }
+        __syncthreads();
+        if (lane == 0) *flag = *reinterpret_cast<volatile int*>(s_status);
+        return;
+    }
+
+    // ================================================================ consumers
+    uint32_t cph = 0, stage = 0, fph = 0;
+    auto csync = [&]() -> bool {                         // a bounded barrier of the consumer warps
+        mbar_arrive(bar(ST_CONS));
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar(ST_CONS), cph, abort_flag, s_status));
+        cph ^= 1;
+        return ok;
+    };
     StepSeg sg;
-    for (bool first = true; step_next<NT>(p, walk, sg, TL::tile); first = false) {
+    bool alive = true;
+    for (bool first = true; alive && step_next<NT>(p, walk, sg, TL::tile); first = false) {
         const int head = sg.head, p0 = sg.p0, nrows = sg.nrows;
         int lo, hi;
         see(sg, &lo, &hi);
-        __syncthreads();                                 // the last pair's q~ and parts are read
 
         // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
         if (warp < 2 * NT) {
@@ -437,15 +488,15 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             *reinterpret_cast<uint4*>(qd) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4*>(qd + 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        __syncthreads();
+        if (!csync()) break;
         // B fragments of q~ (head j, the lane's channels)
         uint32_t qf[NT][16];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                // 16-bit: chunk 4 x + i of 8 channels; 8-bit: the x % 2 half of chunk 4 (x / 2) + i of 16
-                const int ch = FP8 ? ((x >> 1) * 4 + i) * 16 + (x & 1) * 8 : (x * 4 + i) * 8;
+                // 16-bit: chunk 2 i + x % 2 of half x / 2; 8-bit: the x % 2 half of chunk 2 i + x / 2
+                const int ch = FP8 ? (2 * i + (x >> 1)) * 16 + (x & 1) * 8 : (x >> 1) * 64 + (2 * i + (x & 1)) * 8;
                 const uint4 v = lds16(sb + S::q + ((nt * kGroup + j) * kHD + ch) * 2);
                 qf[nt][4 * x] = v.x;
                 qf[nt][4 * x + 1] = v.y;
@@ -462,16 +513,24 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
         }
-        int key0 = (lo & ~15) + sg.t0 * TL::tile + warp * TL::block;
+        int key0 = step_base(p, lo, TL::tile) + sg.t0 * TL::tile + warp * TL::block;
         for (int it = sg.t0; it < sg.t1; ++it, key0 += TL::tile) {
-            // the tile after next, into the buffer read in the last iteration
-            issue(stage >= 1 ? stage - 1 : kStepStages - 1);
-            cp_wait<kStepStages - 1>();
-            if (FP8) __syncwarp();                        // the scales were fetched by other lanes
-            const uint32_t src = ring + stage * kStepStageBytes;
-            const uint8_t* ssc = smem + S::scales + (warp * kStepStages + stage) * 64;
-            if (++stage == kStepStages) stage = 0;
-            if (key0 >= hi || key0 + TL::block <= lo) continue;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(ST_FULL + stage), fph, abort_flag, s_status))) { alive = false; break; }
+            const uint32_t src = sb + S::ring + stage * kStepStage + warp * TL::block * 128;
+            const uint8_t* ssc = smem + S::scales + stage * 256 + warp * kSub * 32;
+            // the last tile's stage is given back at the pair's end
+            auto release = [&]() {
+                if (it + 1 == sg.t1) return;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ST_EMPTY + stage));
+                if (++stage == kStepStages) { stage = 0; fph ^= 1; }
+            };
+            if (key0 >= hi || key0 + TL::block <= lo) {
+                release();
+                continue;
+            }
+            // byte offset of 16-byte chunk x of row r of the warp's rows
+            auto at = [&](int r, int x) -> uint32_t { return src + r * 128 + ((x ^ (r & 7)) << 4); };
             // scores: s[u][nt][0..3] = (key j, heads 2i, 2i + 1), (key j + 8, the same)
             float s[kSub][NT][4];
             float ev[kSub][2];
@@ -485,7 +544,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint4 a = lds16(src + x * 512), b = lds16(src + (4 + x) * 512);
+                        const uint32_t k = at(j, 2 * i + (x & 1)) + (x >> 1) * (kStepHalf / 2);
+                        const uint4 a = lds16(k), b = lds16(k + 1024);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_f16(s[u][nt], a.x, b.x, a.y, b.y, qf[nt][4 * x], qf[nt][4 * x + 1]);
@@ -499,7 +559,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 } else {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const uint4 a = lds16(src + u * 4096 + x * 512), b = lds16(src + u * 4096 + (2 + x) * 512);
+                        const uint32_t k = at(j, 2 * i + x) + u * 2048;
+                        const uint4 a = lds16(k), b = lds16(k + 1024);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const uint32_t aw = reg4(a, r), bw = reg4(b, r);
@@ -521,7 +582,8 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 }
             }
             // masks: only where some row does not see the whole block
-            if (key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window)) {
+            const bool edge = key0 < lo || key0 + TL::block > p0 + 1 || (p.window > 0 && key0 < hi - p.window);
+            if (edge) {
 #pragma unroll
                 for (int u = 0; u < kSub; ++u) {
 #pragma unroll
@@ -541,6 +603,15 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     }
                 }
             }
+            // values in slots that hold no key: anything, NaN included
+            auto drop = [&](uint4& v0, uint4& v1, uint4& v2, uint4& v3, int u) {
+                const int k = key0 + 16 * u + 2 * i;
+                const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                if (k < lo || k >= hi) v0 = z;
+                if (k + 1 < lo || k + 1 >= hi) v1 = z;
+                if (k + 8 < lo || k + 8 >= hi) v2 = z;
+                if (k + 9 < lo || k + 9 >= hi) v3 = z;
+            };
             // raise the running max where a score passes it by 2^8
             bool up = false;
 #pragma unroll
@@ -603,8 +674,9 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const uint4 v0 = lds16(src + 4096 + (hh * 4 + 0) * 512), v1 = lds16(src + 4096 + (hh * 4 + 1) * 512);
-                        const uint4 v2 = lds16(src + 4096 + (hh * 4 + 2) * 512), v3 = lds16(src + 4096 + (hh * 4 + 3) * 512);
+                        const uint32_t va = at(2 * i, j) + kStepHalf + hh * (kStepHalf / 2), vb = at(2 * i + 1, j) + kStepHalf + hh * (kStepHalf / 2);
+                        uint4 v0 = lds16(va), v1 = lds16(vb), v2 = lds16(va + 1024), v3 = lds16(vb + 1024);
+                        if (edge) drop(v0, v1, v2, v3, u);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const uint32_t a0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5410);
@@ -619,8 +691,9 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                         }
                     }
                 } else {
-                    const uint32_t vs = src + u * 4096 + 2048;
-                    const uint4 v0 = lds16(vs), v1 = lds16(vs + 512), v2 = lds16(vs + 1024), v3 = lds16(vs + 1536);
+                    const uint32_t va = at(2 * i, j) + kStepHalf + u * 2048, vb = at(2 * i + 1, j) + kStepHalf + u * 2048;
+                    uint4 v0 = lds16(va), v1 = lds16(vb), v2 = lds16(va + 1024), v3 = lds16(vb + 1024);
+                    if (edge) drop(v0, v1, v2, v3, u);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const uint32_t x0 = __byte_perm(reg4(v0, r), reg4(v1, r), 0x5140);
@@ -639,11 +712,12 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     }
                 }
             }
+            release();
         }
+        if (!alive) break;
 
-        // ---- the four warps' states into one, in warp order.  A warp's part
-        // goes where it read its last tile; the two tiles on their way for the
-        // next pair are in the other stages.
+        // ---- the four warps' states into one, in warp order, in the stage
+        // they read last (the tiles on their way are in the others)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -655,10 +729,9 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                     s_l[warp * S::rows + nt * kGroup + 2 * i + h] = l[nt][h];
                 }
             }
-        __syncthreads();
-        const int used = stage == 0 ? kStepStages - 1 : stage - 1;
-        float* bufs = reinterpret_cast<float*>(smem + S::ring + used * kStepStageBytes);
-        constexpr int kBufStep = kStepStages * kStepStageBytes / 4;       // floats between two warps' stages
+        if (!csync()) break;
+        float* bufs = reinterpret_cast<float*>(smem + S::ring + stage * kStepStage);
+        constexpr int kBufStep = S::rows * kHD;
         float* buf = bufs + warp * kBufStep;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -697,7 +770,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 dst[kPagedStepRows + tid] = l4;
             }
         }
-        __syncthreads();
+        if (!csync()) break;
         // warp w: rows w, w + 4, ..; a lane four channels
 #pragma unroll
         for (int r0 = 0; r0 < S::rows; r0 += kStepWarps) {
@@ -720,10 +793,14 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
                 *reinterpret_cast<float4*>(dst + 2 * kPagedStepRows + r * kHD + 4 * lane) = o;
             }
         }
+        // the parts are read: the stage goes back (the producer's copies into
+        // it follow these generic accesses)
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(ST_EMPTY + stage));
+        if (++stage == kStepStages) { stage = 0; fph ^= 1; }
     }
-    cp_wait<0>();
-    __syncthreads();
-    if (tid == 0) *reinterpret_cast<int*>(p.ws + L.flags + sizeof(int) * blockIdx.x) = *s_bad;
+    __syncthreads();                                     // the producer writes the CTA's flag
 }
 
 // Folds the parts of the pairs that several CTAs hold, in CTA order; block x:
@@ -731,7 +808,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm) paged_step_kerne
 // to do so.  A warp takes a row (block y: rows 4 y .. + 3), a lane four
 // channels.  Block (0, 0) also collects the CTAs' flags into the status word.
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kStepThreads, 4) paged_fold_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kFoldThreads, 4) paged_fold_kernel(const PagedAttnParams p) {
     __shared__ StepPlanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedCache& c = p.c;
@@ -741,19 +818,19 @@ __global__ void __launch_bounds__(kStepThreads, 4) paged_fold_kernel(const Paged
     StepWalk walk;
     long long W, G;
     bool bad;
-    const bool work = step_plan<NT>(p, StepTile<FP8>::tile, blockIdx.x + 1, p.step_ctas, &sm, walk, &W, &G, &bad);
+    const bool work = step_plan<NT, kFoldThreads>(p, StepTile<FP8>::tile, blockIdx.x + 1, p.step_ctas, &sm, walk, &W, &G, &bad);
     griddep_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
-        bool any = bad;
-        for (int x = tid; x < p.step_ctas; x += kStepThreads) any = any || reinterpret_cast<const int*>(p.ws + L.flags)[x] != 0;
-        if (__syncthreads_or(any) && tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = kStatusInvalid;
-        else if (tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = kStatusOk;
+        int any = bad ? kStatusInvalid : kStatusOk;
+        for (int x = tid; x < p.step_ctas; x += kFoldThreads) any = max(any, reinterpret_cast<const int*>(p.ws + L.flags)[x]);
+        const bool timeout = __syncthreads_or(any == kStatusTimeout), invalid = __syncthreads_or(any != kStatusOk);
+        if (tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = timeout ? kStatusTimeout : invalid ? kStatusInvalid : kStatusOk;
     }
     StepSeg sg;
     if (!work || !step_next<NT>(p, walk, sg, StepTile<FP8>::tile) || sg.t0 == 0) return;   // the share begins with a pair
     const PagedParts pp = paged_parts(W, G, W * ((long long)blockIdx.x + 1) / G - sg.t0, sg.tiles);
     if (pp.cf != (int)blockIdx.x) return;                // an earlier block folds this pair
-    const int r = kStepWarps * blockIdx.y + warp;        // the warp's row
+    const int r = (kFoldThreads / 32) * blockIdx.y + warp;   // the warp's row
     if (r < kGroup * sg.nrows) {
         float M = -INFINITY;
         for (int x = pp.cf + lane; x <= pp.cl; x += 32) M = fmaxf(M, part[pp.slot(x) * kStepPart + r]);
@@ -795,8 +872,21 @@ __global__ void __launch_bounds__(kStepThreads, 4) paged_fold_kernel(const Paged
 // ============================================================================ host
 namespace {
 
+// dims (128, ps, rows) of 16-bit elements, or codes; box (128 bytes, slots, 1),
+// 128-byte swizzle.
+flint_status_t step_map(EncodeTiledFn enc, CUtensorMap* m, CUtensorMapDataType dt, int bytes, const void* base, cuuint64_t ps,
+                        cuuint64_t rows, int slots) {
+    cuuint64_t dims[3] = {(cuuint64_t)kHD, ps, rows};
+    cuuint64_t strides[2] = {(cuuint64_t)kHD * bytes, ps * kHD * bytes};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / bytes), (cuuint32_t)slots, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = enc(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(FLINT_ERR_CUDA, "cuTensorMapEncodeTiled (paged step) failed (%d)", (int)r);
+    return FLINT_OK;
+}
+
 template <int NT, bool FP8>
-cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
+cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStream_t s) {
     static bool set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -806,12 +896,12 @@ cudaError_t launch_step(const PagedAttnParams& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
-    paged_step_kernel<NT, FP8><<<p.step_ctas, kStepThreads, StepSmem<NT>::total, s>>>(p);
+    paged_step_kernel<NT, FP8><<<p.step_ctas, kStepThreads, StepSmem<NT>::total, s>>>(maps, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.step_ctas > 1 ? p.step_ctas - 1 : 1, kGroup * NT / kStepWarps);
-    cfg.blockDim = dim3(kStepThreads);
+    cfg.gridDim = dim3(p.step_ctas > 1 ? p.step_ctas - 1 : 1, kGroup * NT / (kFoldThreads / 32));
+    cfg.blockDim = dim3(kFoldThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -836,15 +926,27 @@ size_t paged_attn_workspace(int B, int T, int max_new, int ng) {
 }
 
 flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, cudaStream_t s) {
-    (void)c;
     PagedAttnParams p = in;
     if (sms > kPagedMaxSms) sms = kPagedMaxSms;
     p.step_ctas = sms * kStepCtasPerSm;
     p.chunk_ctas = p.max_new > kStepMaxNew ? sms : 0;
     if (p.chunk_ctas) return launch_paged_chunk(p, s);
     const bool fp8 = p.k_scales != nullptr;
-    const cudaError_t e = p.max_new > 1 ? (fp8 ? launch_step<2, true>(p, s) : launch_step<2, false>(p, s))
-                                        : (fp8 ? launch_step<1, true>(p, s) : launch_step<1, false>(p, s));
+    EncodeTiledFn enc = nullptr;
+    flint_status_t st = get_encoder(&enc);
+    if (st != FLINT_OK) return st;
+    StepMaps m;
+    const cuuint64_t ps = 1u << c.ps_log2, rows = (cuuint64_t)c.num_pages * c.ng;
+    const int tile = fp8 ? StepTile<true>::tile : StepTile<false>::tile, box = (int)ps < tile ? (int)ps : tile, bytes = fp8 ? 1 : 2;
+    const CUtensorMapDataType tk = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapDataType tv = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    st = step_map(enc, &m.k, tk, bytes, p.k_pages, ps, rows, box);
+    if (st == FLINT_OK) st = step_map(enc, &m.v, tv, bytes, p.v_pages, ps, rows, box);
+    if (st == FLINT_OK) st = step_map(enc, &m.k16, tk, bytes, p.k_pages, ps, rows, 16);
+    if (st == FLINT_OK) st = step_map(enc, &m.v16, tv, bytes, p.v_pages, ps, rows, 16);
+    if (st != FLINT_OK) return st;
+    const cudaError_t e = p.max_new > 1 ? (fp8 ? launch_step<2, true>(m, p, s) : launch_step<2, false>(m, p, s))
+                                        : (fp8 ? launch_step<1, true>(m, p, s) : launch_step<1, false>(m, p, s));
     if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return FLINT_OK;
 }
