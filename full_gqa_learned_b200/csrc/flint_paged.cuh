@@ -131,18 +131,45 @@ constexpr int kPagedStepRows = 16;       // query rows of a step partial
 constexpr size_t kStepPart = (size_t)kPagedStepRows * (kHD + 2);
 constexpr size_t kChunkPart = (size_t)8 * kChunkTok * (kHD + 2);
 
-// Workspace of an attention call: of the step kernel (chunk_ctas == 0) a flag
+// The CTA that owns tile x.
+__device__ __forceinline__ long long paged_owner(long long W, long long G, long long x) { return ((x + 1) * G - 1) / W; }
+// The CTAs cf .. cl that hold parts of the pair whose first tile is tile seg
+// of all W, and where they left them: a CTA's first pair in slot 2 c, a later
+// one (its last) in 2 c + 1.  Every CTA but cf begins inside the pair.
+struct PagedParts {
+    int cf, cl;
+    bool second;                 // in cf's share it is not the first pair
+    __device__ __forceinline__ size_t slot(int x) const { return 2 * (size_t)x + (x == cf && second ? 1 : 0); }
+};
+__device__ __forceinline__ PagedParts paged_parts(long long W, long long G, long long seg, int tiles) {
+    PagedParts r;
+    r.cf = (int)paged_owner(W, G, seg);
+    r.cl = (int)paged_owner(W, G, seg + tiles - 1);
+    r.second = W * r.cf / G < seg;
+    return r;
+}
+
+// What a step CTA leaves for the fold kernel.
+struct StepNote {
+    int status;                  // the CTA's
+    int fold;                    // 1: its share is the first to begin inside a pair; the pair:
+    PagedParts parts;
+    int row, head, rows;         // packed row of its first token, KV head, query rows
+    int pad;
+};
+
+// Workspace of an attention call: of the step kernel (chunk_ctas == 0) a note
 // and two partials a CTA, of the chunk kernel the plan and two partials a CTA.
 struct PagedWs {
-    size_t header, flags, spart, inv, groups, prefix, cpart, total;
+    size_t header, notes, spart, inv, groups, prefix, cpart, total;
 };
 __host__ __device__ inline PagedWs paged_ws(int B, int T, int step_ctas, int chunk_ctas) {
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.flags = L.spart = L.inv = L.groups = L.prefix = L.cpart = o;
+    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = o;
     if (chunk_ctas == 0) {
-        o = ws_align(o + sizeof(int) * (size_t)step_ctas, 256);
+        o = ws_align(o + sizeof(StepNote) * (size_t)step_ctas, 256);
         L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
     } else {
         const size_t n = (size_t)T / kChunkTok + (B < T ? B : T);
@@ -223,22 +250,4 @@ __device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g, boo
     if (++s.head == s.ng) { s.head = 0; ++s.gi; }
     return true;
 }
-// The CTA that owns tile x.
-__device__ __forceinline__ long long paged_owner(long long W, long long G, long long x) { return ((x + 1) * G - 1) / W; }
-// The CTAs cf .. cl that hold parts of the pair whose first tile is tile seg
-// of all W, and where they left them: a CTA's first pair in slot 2 c, a later
-// one (its last) in 2 c + 1.  Every CTA but cf begins inside the pair.
-struct PagedParts {
-    int cf, cl;
-    bool second;                 // in cf's share it is not the first pair
-    __device__ __forceinline__ size_t slot(int x) const { return 2 * (size_t)x + (x == cf && second ? 1 : 0); }
-};
-__device__ __forceinline__ PagedParts paged_parts(long long W, long long G, long long seg, int tiles) {
-    PagedParts r;
-    r.cf = (int)paged_owner(W, G, seg);
-    r.cl = (int)paged_owner(W, G, seg + tiles - 1);
-    r.second = W * r.cf / G < seg;
-    return r;
-}
-
 }  // namespace flint

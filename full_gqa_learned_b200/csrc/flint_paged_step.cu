@@ -21,7 +21,9 @@
 //   for any mix of lengths.  Each CTA works its share out from the lengths
 //   (no planning launch in front).  A (group, head) inside one CTA is written
 //   at once; otherwise its CTAs leave partials (m, l, O), folded in CTA order
-//   by the kernel behind (results do not depend on timing).
+//   by the kernel behind (results do not depend on timing).  Folding by the
+//   last CTA to finish, with counters cleared by a kernel in front, took 3 to
+//   6 us a call longer.
 // * A producer warp streams the tiles by TMA (three stages of 32 KiB, two CTAs
 //   an SM), across the pairs of its share: interior tiles in boxes as tall as
 //   a page and tile allow, a pair's edges in boxes of 16 slots, so that next
@@ -62,7 +64,6 @@ flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s);
 
 constexpr int kStepWarps = 4;                            // consumer warps
 constexpr int kStepThreads = 32 * kStepWarps + 32;       // and the producer
-constexpr int kFoldThreads = 128;
 constexpr uint32_t kStepStages = 3;
 constexpr uint32_t kStepHalf = 16384;                    // a tile's keys, or values
 constexpr uint32_t kStepStage = 2 * kStepHalf;
@@ -202,22 +203,26 @@ __device__ __forceinline__ bool step_next(const PagedAttnParams& p, StepWalk& w,
 // The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
 // share them; *bad: ill-formed boundaries or lengths.  Every thread of the
 // block calls it; false: no share.
-struct StepPlanSmem { long long scan[8]; StepWalk walk; int bad; };
-template <int NT, int THREADS>
+struct StepPlanSmem { long long scan[8]; int at[5]; int bad; };
+template <int NT>
 __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas, StepPlanSmem* sm, StepWalk& w, long long* W,
                           long long* G, bool* bad) {
     const PagedCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) sm->bad = c.cu[0] != 0 || c.cu[c.B] > c.T;
-    __syncthreads();
     // a run of sequences a thread
-    const int per = (c.B + THREADS - 1) / THREADS, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+    const int per = (c.B + kStepThreads - 1) / kStepThreads, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+    bool ill = false;
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int len = __ldg(c.len + b);
-        const int n = paged_new(c, p.max_new, __ldg(c.cu + b), __ldg(c.cu + b + 1), len);
-        if (n < 0) sm->bad = 1;
-        for (int r = 0; r < n; r += NT) sum += step_tiles(p, len + r, min(NT, n - r), tile);
+    if (b0 < b1) {
+        int a = __ldg(c.cu + b0);
+        if (b0 == 0) ill = a != 0;
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(c.len + b), z = __ldg(c.cu + b + 1);
+            const int n = paged_new(c, p.max_new, a, z, len);
+            ill = ill || n < 0;                               // a last boundary past T as well
+            for (int r = 0; r < n; r += NT) sum += step_tiles(p, len + r, min(NT, n - r), tile);
+            a = z;
+        }
     }
     long long inc = sum;
 #pragma unroll
@@ -226,14 +231,13 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
         if (lane >= o) inc += y;
     }
     if (lane == 31) sm->scan[warp] = inc;
-    __syncthreads();
+    *bad = __syncthreads_or(ill);
     long long before = inc - sum, total = 0;
 #pragma unroll
-    for (int x = 0; x < THREADS / 32; ++x) {
+    for (int x = 0; x < kStepThreads / 32; ++x) {
         if (x < warp) before += sm->scan[x];
         total += sm->scan[x];
     }
-    *bad = sm->bad != 0;
     *W = total * c.ng;
     *G = *W < (long long)ctas ? *W : (long long)ctas;
     if (cta >= *G) return false;
@@ -252,19 +256,21 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
                 in -= tl * c.ng;
             }
             if (r < n) {
-                StepWalk v;
-                step_enter(p, v, b, a, z, len);
-                v.row0 = r;
-                v.head = (int)(in / tl);
-                v.off = (int)(in - v.head * tl);
-                v.left = (int)(end - t);
-                sm->walk = v;
+                sm->at[0] = b;
+                sm->at[1] = r;
+                sm->at[2] = (int)(in / tl);
+                sm->at[3] = (int)(in % tl);
                 break;
             }
         }
     }
     __syncthreads();
-    w = sm->walk;
+    const int b = sm->at[0];
+    step_enter(p, w, b, __ldg(c.cu + b), __ldg(c.cu + b + 1), __ldg(c.len + b));
+    w.row0 = sm->at[1];
+    w.head = sm->at[2];
+    w.off = sm->at[3];
+    w.left = (int)(end - t);
     return true;
 }
 
@@ -286,7 +292,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     const int ng = c.ng, nh = kGroup * ng;
     const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
-    int* flag = reinterpret_cast<int*>(p.ws + L.flags) + blockIdx.x;
+    StepNote* note = reinterpret_cast<StepNote*>(p.ws + L.notes) + blockIdx.x;
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
     float* s_fin = reinterpret_cast<float*>(smem + S::fin);
@@ -308,8 +314,9 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     StepWalk walk;
     long long W, G;
     bool bad;
-    if (!step_plan<NT, kStepThreads>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad)) {
-        if (tid == 0) *flag = bad ? kStatusInvalid : kStatusOk;
+    const bool work = step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad);
+    if (!work) {
+        if (tid == 0) *note = StepNote{bad ? kStatusInvalid : kStatusOk};
         return;
     }
     if (tid == 0) {
@@ -420,7 +427,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
             if (nl) mbar_wait(bar(ST_FULL + x), (nl - 1) & 1, &never, nullptr, 100ull * 1000ull * 1000ull);
         }
         __syncthreads();
-        if (lane == 0) *flag = *reinterpret_cast<volatile int*>(s_status);
+        if (lane == 0) note->status = *reinterpret_cast<volatile int*>(s_status);
         return;
     }
 
@@ -438,6 +445,23 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         const int head = sg.head, p0 = sg.p0, nrows = sg.nrows;
         int lo, hi;
         see(sg, &lo, &hi);
+        if (first && tid == 0) {
+            // a pair that the share begins inside of is held in part by the
+            // CTAs before, too: the first CTA of those leaves the fold a note
+            StepNote n = {};
+            if (sg.t0 > 0) {
+                n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.tiles);
+                n.fold = n.parts.cf == (int)blockIdx.x - 1;
+                n.row = sg.row;
+                n.head = head;
+                n.rows = kGroup * nrows;
+            }
+            note->fold = n.fold;
+            note->parts = n.parts;
+            note->row = n.row;
+            note->head = n.head;
+            note->rows = n.rows;
+        }
 
         // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
         if (warp < 2 * NT) {
@@ -800,73 +824,70 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         if (lane == 0) mbar_arrive(bar(ST_EMPTY + stage));
         if (++stage == kStepStages) { stage = 0; fph ^= 1; }
     }
-    __syncthreads();                                     // the producer writes the CTA's flag
+    __syncthreads();                                     // the producer records the CTA's status
 }
 
-// Folds the parts of the pairs that several CTAs hold, in CTA order; block x:
-// the pair that CTA x + 1's share begins inside of, if x + 1 is the first CTA
-// to do so.  A warp takes a row (block y: rows 4 y .. + 3), a lane four
-// channels.  Block (0, 0) also collects the CTAs' flags into the status word.
-template <int NT, bool FP8>
+// Folds the parts of the pairs that several CTAs hold, in CTA order: block
+// (x, y) what CTA x + 1's note says, rows 4 y .. 4 y + 3.  A warp takes a row, a
+// lane four channels and every 32nd CTA's weight.  Block (0, 0) also collects
+// the CTAs' statuses.
+constexpr int kFoldThreads = 128;
 __global__ void __launch_bounds__(kFoldThreads, 4) paged_fold_kernel(const PagedAttnParams p) {
-    __shared__ StepPlanSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedCache& c = p.c;
     const int nh = kGroup * c.ng;
     const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
+    const StepNote* notes = reinterpret_cast<const StepNote*>(p.ws + L.notes);
     const float* part = reinterpret_cast<const float*>(p.ws + L.spart);
-    StepWalk walk;
-    long long W, G;
-    bool bad;
-    const bool work = step_plan<NT, kFoldThreads>(p, StepTile<FP8>::tile, blockIdx.x + 1, p.step_ctas, &sm, walk, &W, &G, &bad);
     griddep_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
-        int any = bad ? kStatusInvalid : kStatusOk;
-        for (int x = tid; x < p.step_ctas; x += kFoldThreads) any = max(any, reinterpret_cast<const int*>(p.ws + L.flags)[x]);
+        int any = kStatusOk;
+        for (int x = tid; x < p.step_ctas; x += kFoldThreads) any = max(any, notes[x].status);
         const bool timeout = __syncthreads_or(any == kStatusTimeout), invalid = __syncthreads_or(any != kStatusOk);
         if (tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = timeout ? kStatusTimeout : invalid ? kStatusInvalid : kStatusOk;
     }
-    StepSeg sg;
-    if (!work || !step_next<NT>(p, walk, sg, StepTile<FP8>::tile) || sg.t0 == 0) return;   // the share begins with a pair
-    const PagedParts pp = paged_parts(W, G, W * ((long long)blockIdx.x + 1) / G - sg.t0, sg.tiles);
-    if (pp.cf != (int)blockIdx.x) return;                // an earlier block folds this pair
-    const int r = (kFoldThreads / 32) * blockIdx.y + warp;   // the warp's row
-    if (r < kGroup * sg.nrows) {
-        float M = -INFINITY;
-        for (int x = pp.cf + lane; x <= pp.cl; x += 32) M = fmaxf(M, part[pp.slot(x) * kStepPart + r]);
+    if ((int)blockIdx.x + 1 >= p.step_ctas) return;
+    const StepNote n = notes[blockIdx.x + 1];
+    const int r = (kFoldThreads / 32) * blockIdx.y + warp;    // the warp's row
+    if (!n.fold || r >= n.rows) return;
+    const PagedParts pp = n.parts;
+    float M = -INFINITY;
+    for (int x = pp.cf + lane; x <= pp.cl; x += 32) M = fmaxf(M, __ldcg(part + pp.slot(x) * kStepPart + r));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAhead = 12;                       // parts on their way at once
-        for (int x0 = pp.cf; x0 <= pp.cl; x0 += kAhead) {
-            float mx[kAhead], lx[kAhead];
-            float4 v[kAhead];
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float lsum = 0.f;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = pp.cf; x0 <= pp.cl; x0 += 32) {
+        const int xl = min(x0 + lane, pp.cl), cnt = min(32, pp.cl - x0 + 1);
+        const float mx = __ldcg(part + pp.slot(xl) * kStepPart + r);
+        const float lx = __ldcg(part + pp.slot(xl) * kStepPart + kPagedStepRows + r);
+        const float a = mx > -INFINITY && lane < cnt ? exp2f(mx - M) : 0.f;
+        lsum += lx * a;
+        for (int k0 = 0; k0 < cnt; k0 += 16) {               // sixteen parts on their way at once
+            float4 v[16];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const float* b = part + pp.slot(min(x0 + k, pp.cl)) * kStepPart;
-                mx[k] = __ldcg(b + r);
-                lx[k] = __ldcg(b + kPagedStepRows + r);
-                v[k] = __ldcg(reinterpret_cast<const float4*>(b + 2 * kPagedStepRows + r * kHD) + lane);
-            }
+            for (int k = 0; k < 16; ++k)
+                v[k] = __ldcg(reinterpret_cast<const float4*>(part + pp.slot(min(x0 + k0 + k, pp.cl)) * kStepPart +
+                                                              2 * kPagedStepRows + r * kHD) + lane);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const float a = mx[k] > -INFINITY && x0 + k <= pp.cl ? exp2f(mx[k] - M) : 0.f;
-                l += lx[k] * a;
-                o.x += v[k].x * a;
-                o.y += v[k].y * a;
-                o.z += v[k].z * a;
-                o.w += v[k].w * a;
+            for (int k = 0; k < 16; ++k) {
+                const float ak = __shfl_sync(0xffffffffu, a, k0 + k);
+                o4.x += v[k].x * ak;
+                o4.y += v[k].y * ak;
+                o4.z += v[k].z * ak;
+                o4.w += v[k].w * ak;
             }
         }
-        const int h = kGroup * sg.head + (r & 7);
-        const size_t row = (size_t)sg.row + (r >> 3);
-        float sc, lse;
-        paged_finish(M, l, p.sinks[h], &sc, &lse);
-        *reinterpret_cast<uint2*>(p.out + (row * nh + h) * kHD + 4 * lane) =
-            make_uint2(pack2_bf16(o.x * sc, o.y * sc), pack2_bf16(o.z * sc, o.w * sc));
-        if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + row] = lse;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, o);
+    const int h = kGroup * n.head + (r & 7);
+    const size_t row = (size_t)n.row + (r >> 3);
+    float sc, v;
+    paged_finish(M, lsum, p.sinks[h], &sc, &v);
+    *reinterpret_cast<uint2*>(p.out + (row * nh + h) * kHD + 4 * lane) =
+        make_uint2(pack2_bf16(o4.x * sc, o4.y * sc), pack2_bf16(o4.z * sc, o4.w * sc));
+    if (lane == 0 && p.lse) p.lse[(size_t)h * c.T + row] = v;
 }
 
 // ============================================================================ host
@@ -897,7 +918,7 @@ cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStre
         set[dev & 63] = true;
     }
     paged_step_kernel<NT, FP8><<<p.step_ctas, kStepThreads, StepSmem<NT>::total, s>>>(maps, p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.step_ctas > 1 ? p.step_ctas - 1 : 1, kGroup * NT / (kFoldThreads / 32));
@@ -908,7 +929,7 @@ cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_fold_kernel<NT, FP8>, p);
+    return cudaLaunchKernelEx(&cfg, paged_fold_kernel, p);
 }
 
 // The workspace does not depend on the device: room for a full B200's CTAs.
