@@ -304,13 +304,6 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     auto bar = [&](uint32_t x) { return sb + S::bar + 8 * x; };
 
     griddep_launch_dependents();                         // the fold kernel, which waits for this one
-    const float mq = warp_max_abs128(p.q_norm_w);
-    const int eq = prescale_exponent(mq);
-    const float C = ldexpf(1.4426950408889634f * 0.08838834764831845f, -eq);   // log2(e) / sqrt(128)
-    const float qscale = ldexpf(1.f, eq);
-    if (tid < kHD) s_w[tid] = p.q_norm_w[tid];
-    if (tid < nh) s_sink[tid] = p.sinks[tid];
-    if (p.use_rope && tid < 64) s_inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     StepWalk walk;
     long long W, G;
     bool bad;
@@ -432,6 +425,13 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     }
 
     // ================================================================ consumers
+    // (their constants are fetched while the first tiles are on their way)
+    const int eq = prescale_exponent(warp_max_abs128(p.q_norm_w));
+    const float C = ldexpf(1.4426950408889634f * 0.08838834764831845f, -eq);   // log2(e) / sqrt(128)
+    const float qscale = ldexpf(1.f, eq);
+    s_w[tid] = p.q_norm_w[tid];
+    if (tid < nh) s_sink[tid] = p.sinks[tid];
+    if (p.use_rope && tid < 64) s_inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     uint32_t cph = 0, stage = 0, fph = 0;
     auto csync = [&]() -> bool {                         // a bounded barrier of the consumer warps
         mbar_arrive(bar(ST_CONS));
@@ -440,7 +440,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         return ok;
     };
     StepSeg sg;
-    bool alive = true;
+    bool alive = csync();
     for (bool first = true; alive && step_next<NT>(p, walk, sg, TL::tile); first = false) {
         const int head = sg.head, p0 = sg.p0, nrows = sg.nrows;
         int lo, hi;
@@ -828,11 +828,11 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
 }
 
 // Folds the parts of the pairs that several CTAs hold, in CTA order: block
-// (x, y) what CTA x + 1's note says, rows 4 y .. 4 y + 3.  A warp takes a row, a
+// (x, y) what CTA x + 1's note says, rows 8 y .. 8 y + 7.  A warp takes a row, a
 // lane four channels and every 32nd CTA's weight.  Block (0, 0) also collects
 // the CTAs' statuses.
-constexpr int kFoldThreads = 128;
-__global__ void __launch_bounds__(kFoldThreads, 4) paged_fold_kernel(const PagedAttnParams p) {
+constexpr int kFoldThreads = 256;
+__global__ void __launch_bounds__(kFoldThreads, 2) paged_fold_kernel(const PagedAttnParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedCache& c = p.c;
     const int nh = kGroup * c.ng;
@@ -851,31 +851,46 @@ __global__ void __launch_bounds__(kFoldThreads, 4) paged_fold_kernel(const Paged
     const int r = (kFoldThreads / 32) * blockIdx.y + warp;    // the warp's row
     if (!n.fold || r >= n.rows) return;
     const PagedParts pp = n.parts;
-    float M = -INFINITY;
-    for (int x = pp.cf + lane; x <= pp.cl; x += 32) M = fmaxf(M, __ldcg(part + pp.slot(x) * kStepPart + r));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float lsum = 0.f;
+    // thirty-two parts a round, their weights a lane each; the running max
+    // (rounds after the first) rescales what is there
+    float M = -INFINITY, lsum = 0.f;
     float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x0 = pp.cf; x0 <= pp.cl; x0 += 32) {
         const int xl = min(x0 + lane, pp.cl), cnt = min(32, pp.cl - x0 + 1);
         const float mx = __ldcg(part + pp.slot(xl) * kStepPart + r);
         const float lx = __ldcg(part + pp.slot(xl) * kStepPart + kPagedStepRows + r);
-        const float a = mx > -INFINITY && lane < cnt ? exp2f(mx - M) : 0.f;
-        lsum += lx * a;
-        for (int k0 = 0; k0 < cnt; k0 += 16) {               // sixteen parts on their way at once
-            float4 v[16];
+        float4 v[16];                                        // sixteen parts on their way at once
+        auto load = [&](int k0) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-                v[k] = __ldcg(reinterpret_cast<const float4*>(part + pp.slot(min(x0 + k0 + k, pp.cl)) * kStepPart +
-                                                              2 * kPagedStepRows + r * kHD) + lane);
+                if (k0 + k < cnt)
+                    v[k] = __ldcg(reinterpret_cast<const float4*>(part + pp.slot(x0 + k0 + k) * kStepPart +
+                                                                  2 * kPagedStepRows + r * kHD) + lane);
+        };
+        load(0);
+        float Mn = fmaxf(M, mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+        const float back = M > -INFINITY ? exp2f(M - Mn) : 0.f;
+        M = Mn;
+        lsum *= back;
+        o4.x *= back;
+        o4.y *= back;
+        o4.z *= back;
+        o4.w *= back;
+        const float a = mx > -INFINITY && lane < cnt ? exp2f(mx - M) : 0.f;
+        lsum += lx * a;
+        for (int k0 = 0; k0 < cnt; k0 += 16) {
+            if (k0) load(k0);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const float ak = __shfl_sync(0xffffffffu, a, k0 + k);
-                o4.x += v[k].x * ak;
-                o4.y += v[k].y * ak;
-                o4.z += v[k].z * ak;
-                o4.w += v[k].w * ak;
+                if (k0 + k < cnt) {
+                    o4.x += v[k].x * ak;
+                    o4.y += v[k].y * ak;
+                    o4.z += v[k].z * ak;
+                    o4.w += v[k].w * ak;
+                }
             }
         }
     }
