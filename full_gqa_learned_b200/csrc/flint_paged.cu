@@ -249,7 +249,7 @@ struct ReadParams {
 };
 
 __device__ __forceinline__ float2 paged_decode2(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    const uint32_t h = e4m3_f16(codes);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadPar
                 __nv_bfloat162 vo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 a = paged_decode2((kw[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-                    const float2 b = paged_decode2((vw[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                    const float2 a = paged_decode2(kw[i >> 1] >> (16 * (i & 1)));
+                    const float2 b = paged_decode2(vw[i >> 1] >> (16 * (i & 1)));
                     ko[i] = __floats2half2_rn(a.x * sk, a.y * sk);
                     vo[i] = __floats2bfloat162_rn(b.x * sv, b.y * sv);
                 }

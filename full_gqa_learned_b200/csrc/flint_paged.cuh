@@ -81,6 +81,13 @@ __device__ __forceinline__ float paged_scale(uint32_t byte) {
     return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(byte << 23);
 }
 
+// The two E4M3 codes in the low half of a word as two FP16 values (exact).
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
+    return r;
+}
+
 // ---- attention of new tokens ------------------------------------------------
 struct PagedAttnParams {
     const __nv_bfloat16* q;      // [T, 8 ng, 128]

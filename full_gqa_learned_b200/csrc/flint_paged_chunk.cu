@@ -31,7 +31,6 @@
 //   stays within 2^8.  A group of at most 16 rows runs on one tile alone.
 // Every wait is bounded (FLINT_ERR_TIMEOUT in the status word, abort, drain).
 #include <cuda.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <cmath>
 
@@ -598,8 +597,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)((cw[e >> 1] >> (16 * (e & 1))) & 0xffffu), __NV_E4M3);
+                        const uint32_t v = e4m3_f16(cw[e >> 1] >> (16 * (e & 1)));
                         const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&v), s2);
                         h[e] = *reinterpret_cast<const uint32_t*>(&y);
                     }
@@ -619,8 +617,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const __half2_raw v = __nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)((cw[e >> 1] >> (16 * (e & 1))) & 0xffffu), __NV_E4M3);
+                        const uint32_t v = e4m3_f16(cw[e >> 1] >> (16 * (e & 1)));
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
                         h[e] = pc_pack_bf16(f.x * s, f.y * s);
                     }

@@ -112,12 +112,6 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// the two E4M3 codes in the low half of a word -> two FP16 values (exact)
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t codes) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
-    return r;
-}
 __device__ __forceinline__ uint32_t reg4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 template <int NT>
