@@ -92,7 +92,7 @@ def load_library() -> ctypes.CDLL:
         lib.flint_paged_read.restype = ctypes.c_int
         lib.flint_paged_read.argtypes = [P] * 7 + [I32] * 6 + [P, P, P, ctypes.c_size_t, P]
         lib.flint_attn_paged_workspace_bytes.restype = ctypes.c_size_t
-        lib.flint_attn_paged_workspace_bytes.argtypes = [I32, I32, I32, I32]
+        lib.flint_attn_paged_workspace_bytes.argtypes = [I32] * 8
         lib.flint_attn_paged.restype = ctypes.c_int
         lib.flint_attn_paged.argtypes = [P] * 10 + [I32] * 9 + [F32, F32, P, P, P, ctypes.c_size_t, P]
         lib.flint_attn_device_status.restype = ctypes.c_int
@@ -249,8 +249,11 @@ def attn_decode(q, k, v, q_norm_w, k_norm_w, sinks, k_cache, v_cache, cache_len,
     return out, lse
 
 
-def paged_workspace_bytes(B: int, T: int, max_new: int, kv_heads: int = HKV) -> int:
-    return int(load_library().flint_attn_paged_workspace_bytes(int(B), int(T), int(max_new), int(kv_heads)))
+def paged_workspace_bytes(B: int, T: int, max_new: int, max_pages: int, page_size: int, *, kv_heads: int = HKV,
+                          window: int = 513, eight_bit: bool = False) -> int:
+    return int(load_library().flint_attn_paged_workspace_bytes(int(B), int(T), int(max_new), int(max_pages),
+                                                               int(page_size), int(kv_heads), int(window),
+                                                               int(bool(eight_bit))))
 
 
 def _check_on(dev, **tensors):
@@ -414,7 +417,8 @@ def attn_paged(q, q_norm_w, sinks, k_pages, v_pages, page_table, cache_len, cu_n
         lse = torch.empty((nh, T), dtype=torch.float32, device=dev)
         own.append(lse)
     if workspace is None:
-        workspace = torch.empty(max(paged_workspace_bytes(B, T, max_new, g), 256), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(256, paged_workspace_bytes(
+            B, T, max_new, int(page_table.shape[1]), ps, kv_heads=g, window=window, eight_bit=k_scales is not None)), dtype=torch.uint8, device=dev)
         own.append(workspace)
     _check(out, "out", torch.bfloat16, (T, nh * HEAD_DIM))
     if lse is not None:

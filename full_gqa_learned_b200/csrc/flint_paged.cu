@@ -316,8 +316,9 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadPar
 }
 
 // ============================================================================ host
-flint_status_t launch_paged_attn(const PagedAttnParams& p, const PagedCache& c, int sms, cudaStream_t s);
-size_t paged_attn_workspace(int B, int T, int max_new, int ng);
+flint_status_t launch_paged_attn(const PagedAttnParams& p, const PagedCache& c, int sms, size_t workspace_bytes,
+                                 cudaStream_t s);
+size_t paged_attn_workspace(int B, int T, int max_new, int max_pages, int page_size, int ng, int window, bool fp8);
 
 namespace {
 
@@ -482,11 +483,13 @@ flint_status_t flint_paged_read(const void* k_pages, const void* v_pages, const 
     return FLINT_OK;
 }
 
-size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new, int32_t kv_heads) {
-    if (B < 0 || B > FLINT_MAX_DECODE_BATCH || T < 0 || T > FLINT_MAX_TOKENS || max_new < 0 ||
-        (kv_heads != 1 && kv_heads != 2 && kv_heads != 4))
+size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new, int32_t max_pages, int32_t page_size,
+                                        int32_t kv_heads, int32_t window, int32_t eight_bit) {
+    if (B < 0 || B > FLINT_MAX_DECODE_BATCH || T < 0 || T > FLINT_MAX_TOKENS || max_new < 0 || max_pages < 1 ||
+        max_pages > FLINT_MAX_TOKENS || window < 0 || (kv_heads != 1 && kv_heads != 2 && kv_heads != 4) ||
+        (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128))
         return 0;
-    return paged_attn_workspace(B, T, max_new, kv_heads);
+    return paged_attn_workspace(B, T, max_new, max_pages, page_size, kv_heads, window, eight_bit != 0);
 }
 
 flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const float* sinks, const void* k_pages,
@@ -508,7 +511,9 @@ flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const floa
     if (!q || !q_norm_w || !sinks || !out) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
     if (!al(q, 16) || !al(out, 16)) return fail(FLINT_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
     if (!al(q_norm_w, 4) || !al(sinks, 4) || !al(lse, 4)) return fail(FLINT_ERR_INVALID_ARG, "misaligned 32-bit array");
-    st = check_workspace(workspace, workspace_bytes, paged_attn_workspace(B, T, max_new, kv_heads));
+    // the least: 8-bit pages converted on chip
+    st = check_workspace(workspace, workspace_bytes,
+                         paged_attn_workspace(B, T, max_new, max_pages, page_size, kv_heads, window, false));
     if (st != FLINT_OK) return st;
     int sms = 0;
     st = device_setup(&sms);
@@ -530,7 +535,7 @@ flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const floa
     p.use_rope = use_rope;
     p.rope_theta = rope_theta;
     p.eps = eps;
-    return launch_paged_attn(p, c, sms, static_cast<cudaStream_t>(stream));
+    return launch_paged_attn(p, c, sms, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -103,6 +103,7 @@ struct PagedAttnParams {
     PagedCache c;
     int max_new, window, use_rope;
     int step_ctas, chunk_ctas;   // CTAs of the two kernels (chunk: 0 where it is not run)
+    int stage_rows;              // positions there is room to expand to 16 bits (0: none)
     float rope_theta, eps;
 };
 
@@ -113,6 +114,7 @@ struct PagedGroup {
     int b, nrows, tiles;
     int p0;                      // position of its first row
     int row;                     // packed row of its first row
+    int krow;                    // expanded row of its first chunk's first position
 };
 
 // The work of one kernel: the tiles of all (group, KV head) pairs in a row,
@@ -127,7 +129,8 @@ struct PagedPlanHeader {
     int status;                  // device-side status (0 = ok)
     int pad0;
     PagedList chunk;
-    int pad[58];
+    int stage_rows;              // expanded rows of all sequences
+    int pad[57];
 };
 static_assert(sizeof(PagedPlanHeader) == 256, "plan header");
 
@@ -168,13 +171,13 @@ struct StepNote {
 // Workspace of an attention call: of the step kernel (chunk_ctas == 0) a note
 // and two partials a CTA, of the chunk kernel the plan and two partials a CTA.
 struct PagedWs {
-    size_t header, notes, spart, inv, groups, prefix, cpart, total;
+    size_t header, notes, spart, inv, groups, prefix, cpart, seqrow, stage_k, stage_v, total;
 };
-__host__ __device__ inline PagedWs paged_ws(int B, int T, int step_ctas, int chunk_ctas) {
+__host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas, int chunk_ctas, int stage_rows) {
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = o;
+    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = L.seqrow = L.stage_k = L.stage_v = o;
     if (chunk_ctas == 0) {
         o = ws_align(o + sizeof(StepNote) * (size_t)step_ctas, 256);
         L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
@@ -184,6 +187,11 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int step_ctas, int chu
         L.groups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
         L.prefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
         L.cpart = o;  o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
+        if (stage_rows > 0) {
+            L.seqrow = o;  o = ws_align(o + sizeof(int) * ((size_t)B + 1), 256);
+            L.stage_k = o; o += (size_t)stage_rows * ng * kHD * 2;
+            L.stage_v = o; o += (size_t)stage_rows * ng * kHD * 2;
+        }
     }
     L.total = o;
     return L;

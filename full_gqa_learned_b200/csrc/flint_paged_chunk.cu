@@ -18,10 +18,12 @@
 //   past the last position are not loaded.  Warp 2 writes zeros over the V
 //   rows that hold no position of the group (stale slots may hold NaN, and
 //   0 x NaN would reach every row); masked columns of S need no such care.
-// * 8-bit pages: a third warpgroup reads codes and scales (16 bytes a lane,
-//   whole 128-byte rows), and writes K x 2^e in FP16 and V x 2^e in BF16,
-//   both exact, in the swizzled layout the tensor core reads.  The rest of
-//   the kernel does not know.
+// * 8-bit pages: where the workspace has room, a kernel in front expands the
+//   positions the call reads (codes x 2^e: K in FP16, V in BF16, both exact)
+//   into rows of their own, loaded like pages of any size.  Otherwise a third
+//   warpgroup does the same chunk by chunk, into the swizzled layout that the
+//   tensor core reads; it does so again for every group of 32 tokens, and four
+//   warps need 6 to 9 us a chunk where the products and the softmax take 4.
 // * Warp 1 issues S = Q K^T and O += P V per chunk and tile; warps 4-7 and
 //   8-11 are the softmax warpgroups of the two tiles (one thread a row): RMS
 //   norm and rotation of the queries in place as FP16 when a tile lands, then
@@ -73,6 +75,8 @@ struct PcMisc {
 
 // Threads and registers: 384 threads x 168 launched (8-bit pages: 512 x 128);
 // the control warps give theirs to the softmax warpgroups.
+// Where a chunk's keys and values come from.
+enum PcSource { kPcPages, kPcCodes, kPcStaged };
 template <bool FP8> struct PcShape {
     static constexpr int threads = FP8 ? 512 : 384;
     static constexpr uint32_t control = FP8 ? 40 : 80, softmax = FP8 ? 184 : 208, convert = 104;
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     __shared__ long long sh_l[32];
     const int tid = threadIdx.x;
     const PagedCache& c = p.c;
-    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
     double* inv = reinterpret_cast<double*>(p.ws + L.inv);
     PagedGroup* groups = reinterpret_cast<PagedGroup*>(p.ws + L.groups);
@@ -182,17 +186,38 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     __syncthreads();
     const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
-    int n_groups = 0;
+    int* seqrow = reinterpret_cast<int*>(p.ws + L.seqrow);
+    const int page_mask = (1 << c.ps_log2) - 1;
+    // first position of a page that a sequence's new tokens see, and the rows
+    // from there that are expanded
+    auto span_of = [&](int b, int n, int* base) -> int {
+        const int len = c.len[b], first = p.window > 0 ? max(0, len - p.window + 1) : 0;
+        *base = first & ~page_mask;
+        return n > 0 ? (len + n - *base + 15) & ~15 : 0;
+    };
+    int n_groups = 0, n_rows = 0;
     for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
         const int b1 = b0 + tid * every;
-        int cnt = 0;
+        int cnt = 0, rows = 0, base;
         bool bad = false;
-        for (int b = b1; b < min(b1 + every, c.B); ++b) cnt += (plan_new(p, b, &bad) + kChunkTok - 1) / kChunkTok;
+        for (int b = b1; b < min(b1 + every, c.B); ++b) {
+            const int n = plan_new(p, b, &bad);
+            cnt += (n + kChunkTok - 1) / kChunkTok;
+            if (p.stage_rows > 0) rows += span_of(b, n, &base);
+        }
         if (bad) s_bad = 1;
         int tot;
         const int ex = plan_scan(cnt, sh_i, &tot);
         if (b1 < c.B) off[b1 / every] = n_groups + ex;
         n_groups += tot;
+        if (p.stage_rows > 0) {
+            int at = n_rows + plan_scan(rows, sh_i, &tot);
+            for (int b = b1; b < min(b1 + every, c.B); ++b) {
+                seqrow[b] = at;
+                at += span_of(b, plan_new(p, b, &bad), &base);
+            }
+            n_rows += tot;
+        }
     }
     __syncthreads();
     const int n_off = (c.B + every - 1) / every;
@@ -217,7 +242,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
                     r.p0 = c.len[b] + row0;
                     r.row = c.cu[b] + row0;
                     const int first = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
-                    r.tiles = (r.p0 + r.nrows - (first & ~((1 << c.ps_log2) - 1)) + kKeyChunk - 1) / kKeyChunk;
+                    r.tiles = (r.p0 + r.nrows - (first & ~page_mask) + kKeyChunk - 1) / kKeyChunk;
+                    if (p.stage_rows > 0) {
+                        int base;
+                        span_of(b, n, &base);
+                        r.krow = seqrow[b] + (first & ~page_mask) - base;
+                    }
                     break;
                 }
                 at += k;
@@ -233,9 +263,71 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     }
     if (tid == 0) {
         prefix[n_groups] = tiles;
+        if (p.stage_rows > 0) seqrow[c.B] = n_rows;
+        hdr->stage_rows = n_rows;
         hdr->chunk.n = n_groups;
         hdr->chunk.tiles = tiles;
         hdr->status = s_bad ? kStatusInvalid : kStatusOk;
+    }
+}
+
+// ---------------------------------------------------------------- expansion of 8-bit pages
+// A warp takes 16 positions of one sequence and all heads: eight lanes a row,
+// 16 codes a lane.  Rows without a position are not written (the chunk kernel
+// masks them and clears their values).  It moves 258 bytes in and 512 out per
+// position and head.
+constexpr int kExpandThreads = 256;
+__global__ void __launch_bounds__(kExpandThreads) paged_expand_kernel(const PagedAttnParams p) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, rl = lane >> 3, sub = lane & 7;
+    const PagedCache& c = p.c;
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
+    PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
+    const int* seqrow = reinterpret_cast<const int*>(p.ws + L.seqrow);
+    __half* ks = reinterpret_cast<__half*>(p.ws + L.stage_k);
+    __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(p.ws + L.stage_v);
+    const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
+    const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
+    griddep_wait();
+    const int blocks = min(hdr->stage_rows, p.stage_rows) / 16, warps = gridDim.x * (kExpandThreads / 32);
+    for (int x = blockIdx.x * (kExpandThreads / 32) + (threadIdx.x >> 5); x < blocks; x += warps) {
+        const int b = warp_last_leq(seqrow, c.B, 16 * x);
+        const int len = c.len[b], end = len + c.cu[b + 1] - c.cu[b];
+        const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
+        const int pos = (lo & ~((1 << c.ps_log2) - 1)) + 16 * x - seqrow[b];
+        if (pos >= end || pos + 16 <= lo) continue;
+        const int page = __ldg(c.table + (size_t)b * c.max_pages + (pos >> c.ps_log2));
+        if (page < 0 || page >= c.num_pages) {
+            if (lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
+            continue;
+        }
+        for (int g = 0; g < c.ng; ++g) {
+            const size_t src = paged_row(c, page, g, pos & ((1 << c.ps_log2) - 1)), dst = (size_t)g * p.stage_rows + 16 * x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + rl;
+                if (pos + r < lo || pos + r >= end) continue;
+                const uint4 kc = __ldg(reinterpret_cast<const uint4*>(kp + (src + r) * kHD) + sub);
+                const uint4 vc = __ldg(reinterpret_cast<const uint4*>(vp + (src + r) * kHD) + sub);
+                const float sk = paged_scale(__ldg(p.k_scales + src + r)), sv = paged_scale(__ldg(p.v_scales + src + r));
+                const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+                uint32_t ko[8], vo[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t kh = e4m3_f16(kw[e >> 1] >> (16 * (e & 1))), vh = e4m3_f16(vw[e >> 1] >> (16 * (e & 1)));
+                    const __half2 kk = __hmul2(*reinterpret_cast<const __half2*>(&kh), __float2half2_rn(sk));
+                    const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vh));
+                    ko[e] = *reinterpret_cast<const uint32_t*>(&kk);
+                    vo[e] = pc_pack_bf16(vf.x * sv, vf.y * sv);
+                }
+                uint4* kd = reinterpret_cast<uint4*>(ks + (dst + r) * kHD + 16 * sub);
+                uint4* vd = reinterpret_cast<uint4*>(vs + (dst + r) * kHD + 16 * sub);
+                kd[0] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+                kd[1] = make_uint4(ko[4], ko[5], ko[6], ko[7]);
+                vd[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
+                vd[1] = make_uint4(vo[4], vo[5], vo[6], vo[7]);
+            }
+        }
     }
 }
 
@@ -260,11 +352,12 @@ __device__ __forceinline__ PcGroup pc_group(const PagedAttnParams& p, const Page
 // rounded up to the MMA's step of 16.
 __device__ __forceinline__ int pc_cols(int ks, int hi) { return min(kKeyChunk, (hi - ks + 15) & ~15); }
 
-template <bool FP8>
-__global__ void __launch_bounds__(PcShape<FP8>::threads, 1)
+template <PcSource SRC>
+__global__ void __launch_bounds__(PcShape<SRC == kPcCodes>::threads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                    const __grid_constant__ CUtensorMap tm_o1, const PagedAttnParams p) {
+    constexpr bool FP8 = SRC == kPcCodes;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -274,7 +367,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int* abort_flag = &misc->abort_flag;
     const PagedCache& c = p.c;
     const int ng = c.ng;
-    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
     int* status = &hdr->status;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -359,10 +452,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (FP8 || !ok) continue;
             // lane i < 128 / ps loads page i of each chunk; its table entry is
-            // fetched a chunk ahead
-            const int ps = 1 << c.ps_log2, npg = kKeyChunk >> c.ps_log2;
+            // fetched a chunk ahead.  Expanded rows: one box.
+            const int ps = SRC == kPcStaged ? kKeyChunk : 1 << c.ps_log2, npg = SRC == kPcStaged ? 1 : kKeyChunk >> c.ps_log2;
             const int* table = c.table + (size_t)sg.g.b * c.max_pages;
             auto entry = [&](int ch) -> int {
+                if (SRC == kPcStaged) return lane == 0 ? 0 : -2;
                 const int pos = gr.kb + kKeyChunk * ch + lane * ps;
                 return lane < npg && pos < gr.hi ? __ldg(table + (pos >> c.ps_log2)) : -2;
             };
@@ -373,15 +467,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int page = pg;
                 pg = ch + 1 < sg.t1 ? entry(ch + 1) : -2;
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * ps * kHD * 2;
-                const int z = live ? page * ng + sg.head : 0;
+                const int y = SRC == kPcStaged ? sg.g.krow + kKeyChunk * ch : 0;
+                const int z = SRC == kPcStaged ? sg.head : live ? page * ng + sg.head : 0;
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_K_EMPTY + st), ph ^ 1, abort_flag, status));
                 if (!ok) break;
                 if (lane == 0) mbar_expect_tx(bar(PC_K_FULL + st), bytes);
                 __syncwarp();
                 uint32_t dst = sbase + kPcK + st * kPcTile + lane * ps * 128;
                 if (live) {
-                    tma_load_3d(dst, &tm_k, bar(PC_K_FULL + st), 0, 0, z);
-                    tma_load_3d(dst + kPcHalf, &tm_k, bar(PC_K_FULL + st), 64, 0, z);
+                    tma_load_3d(dst, &tm_k, bar(PC_K_FULL + st), 0, y, z);
+                    tma_load_3d(dst + kPcHalf, &tm_k, bar(PC_K_FULL + st), 64, y, z);
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_EMPTY + st), ph ^ 1, abort_flag, status));
                 if (!ok) {
@@ -393,8 +488,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 dst = sbase + kPcV + st * kPcTile + lane * ps * 128;
                 if (live) {
-                    tma_load_3d(dst, &tm_v, bar(PC_V_FULL + st), 0, 0, z);
-                    tma_load_3d(dst + kPcHalf, &tm_v, bar(PC_V_FULL + st), 64, 0, z);
+                    tma_load_3d(dst, &tm_v, bar(PC_V_FULL + st), 0, y, z);
+                    tma_load_3d(dst + kPcHalf, &tm_v, bar(PC_V_FULL + st), 64, y, z);
                 }
                 ++narm;
                 st ^= 1; if (st == 0) ph ^= 1;
@@ -994,7 +1089,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const PagedCache& c = p.c;
     const int ng = c.ng, nh = kGroup * ng;
-    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, p.chunk_ctas);
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
     const PagedPlanHeader* hdr = reinterpret_cast<const PagedPlanHeader*>(p.ws + L.header);
     const float* part = reinterpret_cast<const float*>(p.ws + L.cpart);
     griddep_wait();
@@ -1061,27 +1156,37 @@ flint_status_t pc_map(EncodeTiledFn enc, CUtensorMap* m, CUtensorMapDataType dt,
     return FLINT_OK;
 }
 
-template <bool FP8>
+template <PcSource SRC>
 cudaError_t launch_chunk(const CUtensorMap* m, const PagedAttnParams& p, cudaStream_t s) {
     static bool set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (!set[dev & 63]) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPcSmem);
+        const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<SRC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPcSmem);
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
+    // each launch a programmatic dependent of the one before it
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.chunk_ctas);
-    cfg.blockDim = dim3(PcShape<FP8>::threads);
-    cfg.dynamicSmemBytes = kPcSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, paged_chunk_kernel<FP8>, m[0], m[1], m[2], m[3], m[4], p);
+    cudaError_t e = cudaSuccess;
+    if (SRC == kPcStaged) {
+        // a warp a block of 16 positions, at most eight blocks an SM
+        const int n = (p.stage_rows / 16 + kExpandThreads / 32 - 1) / (kExpandThreads / 32);
+        cfg.gridDim = dim3(n < 8 * p.chunk_ctas ? n : 8 * p.chunk_ctas);
+        cfg.blockDim = dim3(kExpandThreads);
+        e = cudaLaunchKernelEx(&cfg, paged_expand_kernel, p);
+        if (e != cudaSuccess) return e;
+    }
+    cfg.gridDim = dim3(p.chunk_ctas);
+    cfg.blockDim = dim3(PcShape<SRC == kPcCodes>::threads);
+    cfg.dynamicSmemBytes = kPcSmem;
+    e = cudaLaunchKernelEx(&cfg, paged_chunk_kernel<SRC>, m[0], m[1], m[2], m[3], m[4], p);
     if (e != cudaSuccess || p.chunk_ctas < 2) return e;
     cfg.gridDim = dim3(p.chunk_ctas - 1, 8 * kChunkTok / 32);
     cfg.blockDim = dim3(128);
@@ -1101,15 +1206,25 @@ flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s) {
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap m[5];
     st = pc_map(enc, &m[0], bf, p.q, nh, c.T, kGroup, kTokPerTile);
-    if (st == FLINT_OK && !fp8) st = pc_map(enc, &m[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p.k_pages, ps, rows, (cuuint32_t)ps, 1);
-    if (st == FLINT_OK && !fp8) st = pc_map(enc, &m[2], bf, p.v_pages, ps, rows, (cuuint32_t)ps, 1);
+    const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if (p.stage_rows > 0) {
+        const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
+        if (st == FLINT_OK) st = pc_map(enc, &m[1], f16, p.ws + L.stage_k, p.stage_rows, c.ng, kKeyChunk, 1);
+        if (st == FLINT_OK) st = pc_map(enc, &m[2], bf, p.ws + L.stage_v, p.stage_rows, c.ng, kKeyChunk, 1);
+    } else if (!fp8) {
+        if (st == FLINT_OK) st = pc_map(enc, &m[1], f16, p.k_pages, ps, rows, (cuuint32_t)ps, 1);
+        if (st == FLINT_OK) st = pc_map(enc, &m[2], bf, p.v_pages, ps, rows, (cuuint32_t)ps, 1);
+    } else {
+        m[1] = m[2] = m[0];                         // not used
+    }
     if (st == FLINT_OK) st = pc_map(enc, &m[3], bf, p.out, nh, c.T, kGroup, 4);
     if (st == FLINT_OK) st = pc_map(enc, &m[4], bf, p.out, nh, c.T, kGroup, 1);
     if (st != FLINT_OK) return st;
-    if (fp8) m[1] = m[2] = m[0];                    // not used
     paged_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: plan");
-    const cudaError_t e = fp8 ? launch_chunk<true>(m, p, s) : launch_chunk<false>(m, p, s);
+    const cudaError_t e = p.stage_rows > 0 ? launch_chunk<kPcStaged>(m, p, s)
+                          : fp8            ? launch_chunk<kPcCodes>(m, p, s)
+                                           : launch_chunk<kPcPages>(m, p, s);
     if (e != cudaSuccess) return fail(FLINT_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
     return FLINT_OK;
 }

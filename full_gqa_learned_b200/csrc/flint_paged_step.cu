@@ -284,7 +284,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     const int j = lane >> 2, i = lane & 3;
     const PagedCache& c = p.c;
     const int ng = c.ng, nh = kGroup * ng;
-    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, 0, 0);
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
     StepNote* note = reinterpret_cast<StepNote*>(p.ws + L.notes) + blockIdx.x;
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kFoldThreads, 2) paged_fold_kernel(const Paged
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PagedCache& c = p.c;
     const int nh = kGroup * c.ng;
-    const PagedWs L = paged_ws(c.B, c.T, p.step_ctas, 0);
+    const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, 0, 0);
     const StepNote* notes = reinterpret_cast<const StepNote*>(p.ws + L.notes);
     const float* part = reinterpret_cast<const float*>(p.ws + L.spart);
     griddep_wait();
@@ -948,20 +948,39 @@ constexpr int kPagedMaxSms = 148;
 // kernel, others the chunk kernel.
 constexpr int kStepMaxNew = 8;
 
-}  // namespace
-
-size_t paged_attn_workspace(int B, int T, int max_new, int ng) {
-    (void)ng;
-    return paged_ws(B, T, kPagedMaxSms * kStepCtasPerSm, max_new > kStepMaxNew ? kPagedMaxSms : 0).total;
+// Positions that the chunk kernel's calls on 8-bit pages have expanded to 16
+// bits at most: each sequence's window of its new tokens, from a page's start.
+constexpr size_t kStageMost = (size_t)512 << 20;
+int stage_rows(int B, int T, int max_new, int max_pages, int page_size, int ng, int window) {
+    long long span = (long long)max_pages * page_size;
+    if (span > FLINT_MAX_TOKENS) span = FLINT_MAX_TOKENS;
+    if (window > 0 && span > (long long)window + max_new + page_size) span = (long long)window + max_new + page_size;
+    const long long rows = (span + 15) / 16 * 16 * (B < T ? B : T);
+    return rows * ng * kHD * 4 <= (long long)kStageMost ? (int)rows : 0;
 }
 
-flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, cudaStream_t s) {
+}  // namespace
+
+size_t paged_attn_workspace(int B, int T, int max_new, int max_pages, int page_size, int ng, int window, bool fp8) {
+    const bool chunk = max_new > kStepMaxNew;
+    return paged_ws(B, T, ng, kPagedMaxSms * kStepCtasPerSm, chunk ? kPagedMaxSms : 0,
+                    chunk && fp8 ? stage_rows(B, T, max_new, max_pages, page_size, ng, window) : 0).total;
+}
+
+flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, size_t workspace_bytes,
+                                 cudaStream_t s) {
     PagedAttnParams p = in;
     if (sms > kPagedMaxSms) sms = kPagedMaxSms;
     p.step_ctas = sms * kStepCtasPerSm;
     p.chunk_ctas = p.max_new > kStepMaxNew ? sms : 0;
-    if (p.chunk_ctas) return launch_paged_chunk(p, s);
     const bool fp8 = p.k_scales != nullptr;
+    p.stage_rows = 0;
+    if (p.chunk_ctas) {
+        // 8-bit pages: expanded first where the caller gave room for it
+        const int rows = fp8 ? stage_rows(c.B, c.T, p.max_new, c.max_pages, 1 << c.ps_log2, c.ng, p.window) : 0;
+        if (rows && paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, rows).total <= workspace_bytes) p.stage_rows = rows;
+        return launch_paged_chunk(p, s);
+    }
     EncodeTiledFn enc = nullptr;
     flint_status_t st = get_encoder(&enc);
     if (st != FLINT_OK) return st;

@@ -447,15 +447,21 @@ FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pag
  *  max_new    at least the most new tokens of any sequence (else the device
  *             status becomes FLINT_ERR_INVALID_ARG); chooses the kernels.
  *  out        bf16 [T, 8 kv_heads x 128];  lse  fp32 [8 kv_heads, T] or NULL.
- *  workspace  flint_attn_paged_workspace_bytes(B, T, max_new, kv_heads)
- *             bytes; not shared by calls that may overlap on the GPU.
+ *  workspace  flint_attn_paged_workspace_bytes(...) bytes; not shared by
+ *             calls that may overlap on the GPU.  For 8-bit pages and max_new
+ *             > 8 that counts room (up to 512 MiB, else none) to expand the
+ *             positions the call reads to 16 bits first; a workspace of the
+ *             size for 16-bit pages (eight_bit == 0) is accepted, too: the
+ *             call then converts on chip, with the same result, in about twice
+ *             the time.
  * Cached values and keys at positions a token sees must be finite and scales
  * within 2^-24 .. 2^40; slots of other positions may hold anything, and page
  * table entries that no new token's window touches are not read.
  * Results do not depend on timing: every sum has a fixed order.
  */
 FLINT_API size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new,
-                              int32_t kv_heads);
+                              int32_t max_pages, int32_t page_size, int32_t kv_heads,
+                              int32_t window, int32_t eight_bit);
 FLINT_API flint_status_t flint_attn_paged(const void* q, const float* q_norm_w, const float* sinks,
                               const void* k_pages, const void* v_pages, const void* k_scales,
                               const void* v_scales, const int32_t* page_table,

@@ -181,8 +181,11 @@ def test_chunks(fa, ps, fp8, ctx, new, window):
     st, out, lse = attend(fa, c, t)
     assert st == 0
     check_attend(c, t, out, lse, chunk=True)
-    for _ in range(2):
-        _, o2, l2 = attend(fa, c, t)
+    # again, and in the least workspace (8-bit pages: converted on chip): the same bits
+    least = fa.paged_workspace_bytes(c.B, c.T, int(c.new.max()), c.table.shape[1], ps, window=window)
+    for kw in ({}, {"workspace": torch.empty(least, dtype=torch.uint8, device="cuda")}):
+        st, o2, l2 = attend(fa, c, t, **kw)
+        assert st == 0
         assert torch.equal(out[:c.rows], o2[:c.rows]) and torch.equal(lse[:, :c.rows], l2[:, :c.rows])
 
 
