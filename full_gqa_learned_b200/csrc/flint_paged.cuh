@@ -103,7 +103,7 @@ struct PagedAttnParams {
     PagedCache c;
     int max_new, window, use_rope;
     int step_ctas, chunk_ctas;   // CTAs of the two kernels (chunk: 0 where it is not run)
-    int stage_rows;              // positions there is room to expand to 16 bits (0: none)
+    int stage_rows;              // positions a sequence has room to expand to 16 bits (0: none)
     float rope_theta, eps;
 };
 
@@ -129,8 +129,7 @@ struct PagedPlanHeader {
     int status;                  // device-side status (0 = ok)
     int pad0;
     PagedList chunk;
-    int stage_rows;              // expanded rows of all sequences
-    int pad[57];
+    int pad[58];
 };
 static_assert(sizeof(PagedPlanHeader) == 256, "plan header");
 
@@ -159,9 +158,9 @@ __device__ __forceinline__ PagedParts paged_parts(long long W, long long G, long
     return r;
 }
 
-// What a step CTA leaves for the fold kernel.
-struct StepNote {
-    int status;                  // the CTA's
+// What a CTA leaves for the kernel that folds the parts.
+struct PagedNote {
+    int status;                  // the CTA's (step kernel)
     int fold;                    // 1: its share is the first to begin inside a pair; the pair:
     PagedParts parts;
     int row, head, rows;         // packed row of its first token, KV head, query rows
@@ -171,26 +170,26 @@ struct StepNote {
 // Workspace of an attention call: of the step kernel (chunk_ctas == 0) a note
 // and two partials a CTA, of the chunk kernel the plan and two partials a CTA.
 struct PagedWs {
-    size_t header, notes, spart, inv, groups, prefix, cpart, seqrow, stage_k, stage_v, total;
+    size_t header, notes, spart, inv, groups, prefix, cpart, stage_k, stage_v, total;
 };
 __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas, int chunk_ctas, int stage_rows) {
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = L.seqrow = L.stage_k = L.stage_v = o;
+    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = L.stage_k = L.stage_v = o;
     if (chunk_ctas == 0) {
-        o = ws_align(o + sizeof(StepNote) * (size_t)step_ctas, 256);
+        o = ws_align(o + sizeof(PagedNote) * (size_t)step_ctas, 256);
         L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
     } else {
         const size_t n = (size_t)T / kChunkTok + (B < T ? B : T);
-        o += 64 * sizeof(double);
+        o = ws_align(o + sizeof(PagedNote) * (size_t)chunk_ctas, 256);
+        L.inv = o;    o += 64 * sizeof(double);
         L.groups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
         L.prefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
         L.cpart = o;  o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
         if (stage_rows > 0) {
-            L.seqrow = o;  o = ws_align(o + sizeof(int) * ((size_t)B + 1), 256);
-            L.stage_k = o; o += (size_t)stage_rows * ng * kHD * 2;
-            L.stage_v = o; o += (size_t)stage_rows * ng * kHD * 2;
+            L.stage_k = o; o += (size_t)B * stage_rows * ng * kHD * 2;
+            L.stage_v = o; o += (size_t)B * stage_rows * ng * kHD * 2;
         }
     }
     L.total = o;

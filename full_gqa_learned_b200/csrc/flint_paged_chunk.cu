@@ -186,38 +186,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     __syncthreads();
     const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
-    int* seqrow = reinterpret_cast<int*>(p.ws + L.seqrow);
     const int page_mask = (1 << c.ps_log2) - 1;
-    // first position of a page that a sequence's new tokens see, and the rows
-    // from there that are expanded
-    auto span_of = [&](int b, int n, int* base) -> int {
-        const int len = c.len[b], first = p.window > 0 ? max(0, len - p.window + 1) : 0;
-        *base = first & ~page_mask;
-        return n > 0 ? (len + n - *base + 15) & ~15 : 0;
-    };
-    int n_groups = 0, n_rows = 0;
+    int n_groups = 0;
     for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
         const int b1 = b0 + tid * every;
-        int cnt = 0, rows = 0, base;
+        int cnt = 0;
         bool bad = false;
-        for (int b = b1; b < min(b1 + every, c.B); ++b) {
-            const int n = plan_new(p, b, &bad);
-            cnt += (n + kChunkTok - 1) / kChunkTok;
-            if (p.stage_rows > 0) rows += span_of(b, n, &base);
-        }
+        for (int b = b1; b < min(b1 + every, c.B); ++b) cnt += (plan_new(p, b, &bad) + kChunkTok - 1) / kChunkTok;
         if (bad) s_bad = 1;
         int tot;
         const int ex = plan_scan(cnt, sh_i, &tot);
         if (b1 < c.B) off[b1 / every] = n_groups + ex;
         n_groups += tot;
-        if (p.stage_rows > 0) {
-            int at = n_rows + plan_scan(rows, sh_i, &tot);
-            for (int b = b1; b < min(b1 + every, c.B); ++b) {
-                seqrow[b] = at;
-                at += span_of(b, plan_new(p, b, &bad), &base);
-            }
-            n_rows += tot;
-        }
     }
     __syncthreads();
     const int n_off = (c.B + every - 1) / every;
@@ -244,9 +224,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
                     const int first = p.window > 0 ? max(0, r.p0 - p.window + 1) : 0;
                     r.tiles = (r.p0 + r.nrows - (first & ~page_mask) + kKeyChunk - 1) / kKeyChunk;
                     if (p.stage_rows > 0) {
-                        int base;
-                        span_of(b, n, &base);
-                        r.krow = seqrow[b] + (first & ~page_mask) - base;
+                        const int seq_first = p.window > 0 ? max(0, c.len[b] - p.window + 1) : 0;
+                        r.krow = b * p.stage_rows + (first & ~page_mask) - (seq_first & ~page_mask);
                     }
                     break;
                 }
@@ -263,8 +242,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     }
     if (tid == 0) {
         prefix[n_groups] = tiles;
-        if (p.stage_rows > 0) seqrow[c.B] = n_rows;
-        hdr->stage_rows = n_rows;
         hdr->chunk.n = n_groups;
         hdr->chunk.tiles = tiles;
         hdr->status = s_bad ? kStatusInvalid : kStatusOk;
@@ -272,10 +249,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
 }
 
 // ---------------------------------------------------------------- expansion of 8-bit pages
-// A warp takes 16 positions of one sequence and all heads: eight lanes a row,
-// 16 codes a lane.  Rows without a position are not written (the chunk kernel
-// masks them and clears their values).  It moves 258 bytes in and 512 out per
-// position and head.
+// A warp takes 16 positions of one sequence and KV head: eight lanes a row, 16
+// codes a lane, four rows at once.  Rows without a position are not written (the chunk kernel
+// masks them and clears their values).  Sequence b's rows start at b x
+// stage_rows.  It moves 258 bytes in and 512 out per position and head.
 constexpr int kExpandThreads = 256;
 __global__ void __launch_bounds__(kExpandThreads) paged_expand_kernel(const PagedAttnParams p) {
     griddep_launch_dependents();
@@ -283,52 +260,63 @@ __global__ void __launch_bounds__(kExpandThreads) paged_expand_kernel(const Page
     const PagedCache& c = p.c;
     const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
     PagedPlanHeader* hdr = reinterpret_cast<PagedPlanHeader*>(p.ws + L.header);
-    const int* seqrow = reinterpret_cast<const int*>(p.ws + L.seqrow);
     __half* ks = reinterpret_cast<__half*>(p.ws + L.stage_k);
     __nv_bfloat16* vs = reinterpret_cast<__nv_bfloat16*>(p.ws + L.stage_v);
     const uint8_t* kp = static_cast<const uint8_t*>(p.k_pages);
     const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
-    griddep_wait();
-    const int blocks = min(hdr->stage_rows, p.stage_rows) / 16, warps = gridDim.x * (kExpandThreads / 32);
-    for (int x = blockIdx.x * (kExpandThreads / 32) + (threadIdx.x >> 5); x < blocks; x += warps) {
-        const int b = warp_last_leq(seqrow, c.B, 16 * x);
-        const int len = c.len[b], end = len + c.cu[b + 1] - c.cu[b];
-        const int lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
-        const int pos = (lo & ~((1 << c.ps_log2) - 1)) + 16 * x - seqrow[b];
-        if (pos >= end || pos + 16 <= lo) continue;
+    const int blocks = p.stage_rows / 16, n = c.B * blocks * c.ng, warps = gridDim.x * (kExpandThreads / 32);
+    bool bad = false;
+    for (int w = blockIdx.x * (kExpandThreads / 32) + (threadIdx.x >> 5); w < n; w += warps) {
+        const int b = w / (blocks * c.ng), x = w / c.ng % blocks, g = w % c.ng;
+        const int len = c.len[b], a = c.cu[b], z = c.cu[b + 1], nn = paged_new(c, p.max_new, a, z, len);
+        const int end = len + nn, lo = p.window > 0 ? max(0, len - p.window + 1) : 0;
+        const int pos = (lo & ~((1 << c.ps_log2) - 1)) + 16 * x;
+        if (nn <= 0 || pos >= end || pos + 16 <= lo) continue;
         const int page = __ldg(c.table + (size_t)b * c.max_pages + (pos >> c.ps_log2));
         if (page < 0 || page >= c.num_pages) {
-            if (lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
+            bad = true;
             continue;
         }
-        for (int g = 0; g < c.ng; ++g) {
-            const size_t src = paged_row(c, page, g, pos & ((1 << c.ps_log2) - 1)), dst = (size_t)g * p.stage_rows + 16 * x;
+        const size_t src = paged_row(c, page, g, pos & ((1 << c.ps_log2) - 1)), dst = ((size_t)g * c.B + b) * p.stage_rows + 16 * x;
+        uint4 kc[4], vc[4];
+        uint32_t sk[4], sv[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * i + rl;
-                if (pos + r < lo || pos + r >= end) continue;
-                const uint4 kc = __ldg(reinterpret_cast<const uint4*>(kp + (src + r) * kHD) + sub);
-                const uint4 vc = __ldg(reinterpret_cast<const uint4*>(vp + (src + r) * kHD) + sub);
-                const float sk = paged_scale(__ldg(p.k_scales + src + r)), sv = paged_scale(__ldg(p.v_scales + src + r));
-                const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
-                uint32_t ko[8], vo[8];
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * i + rl;
+            if (pos + r < lo || pos + r >= end) continue;
+            kc[i] = __ldg(reinterpret_cast<const uint4*>(kp + (src + r) * kHD) + sub);
+            vc[i] = __ldg(reinterpret_cast<const uint4*>(vp + (src + r) * kHD) + sub);
+            sk[i] = __ldg(p.k_scales + src + r);
+            sv[i] = __ldg(p.v_scales + src + r);
+        }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t kh = e4m3_f16(kw[e >> 1] >> (16 * (e & 1))), vh = e4m3_f16(vw[e >> 1] >> (16 * (e & 1)));
-                    const __half2 kk = __hmul2(*reinterpret_cast<const __half2*>(&kh), __float2half2_rn(sk));
-                    const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vh));
-                    ko[e] = *reinterpret_cast<const uint32_t*>(&kk);
-                    vo[e] = pc_pack_bf16(vf.x * sv, vf.y * sv);
-                }
-                uint4* kd = reinterpret_cast<uint4*>(ks + (dst + r) * kHD + 16 * sub);
-                uint4* vd = reinterpret_cast<uint4*>(vs + (dst + r) * kHD + 16 * sub);
-                kd[0] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
-                kd[1] = make_uint4(ko[4], ko[5], ko[6], ko[7]);
-                vd[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
-                vd[1] = make_uint4(vo[4], vo[5], vo[6], vo[7]);
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * i + rl;
+            if (pos + r < lo || pos + r >= end) continue;
+            const __half2 ks2 = __float2half2_rn(paged_scale(sk[i]));
+            const float vsf = paged_scale(sv[i]);
+            const uint32_t kw[4] = {kc[i].x, kc[i].y, kc[i].z, kc[i].w}, vw[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w};
+            uint32_t ko[8], vo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t kh = e4m3_f16(kw[e >> 1] >> (16 * (e & 1))), vh = e4m3_f16(vw[e >> 1] >> (16 * (e & 1)));
+                const __half2 kk = __hmul2(*reinterpret_cast<const __half2*>(&kh), ks2);
+                const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vh));
+                ko[e] = *reinterpret_cast<const uint32_t*>(&kk);
+                vo[e] = pc_pack_bf16(vf.x * vsf, vf.y * vsf);
             }
+            uint4* kd = reinterpret_cast<uint4*>(ks + (dst + r) * kHD + 16 * sub);
+            uint4* vd = reinterpret_cast<uint4*>(vs + (dst + r) * kHD + 16 * sub);
+            kd[0] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
+            kd[1] = make_uint4(ko[4], ko[5], ko[6], ko[7]);
+            vd[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
+            vd[1] = make_uint4(vo[4], vo[5], vo[6], vo[7]);
         }
     }
+    // nothing above needs the plan; it writes the status word, and who waits
+    // for this grid waits for it, too
+    griddep_wait();
+    if (bad && lane == 0) atomicCAS(&hdr->status, 0, kStatusInvalid);
 }
 
 // ---------------------------------------------------------------- chunk kernel
@@ -429,6 +417,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (!work) {
         // nothing in flight: straight to the end
+        if (tid == 0) reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = PagedNote{};
     } else if (warp < 4) {
       regs_dec<PcShape<FP8>::control>();
       if (warp == 0) {
@@ -601,6 +590,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_wait(bar(PC_DRAIN), 0, &never, nullptr, 100ull * 1000ull * 1000ull);
         }
         __syncwarp();
+      } else if (warp == 3) {
+        // ============================================================ the note for the combine kernel
+        if (paged_share_next(share, sg, true) && lane == 0) {
+            // a pair that the share begins inside of is held in part by the
+            // CTAs before, too: the first CTA of those leaves the combine a note
+            const long long W = hdr->chunk.tiles * ng, G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
+            PagedNote n = {};
+            if (sg.t0 > 0) {
+                n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.g.tiles);
+                n.fold = n.parts.cf == (int)blockIdx.x - 1;
+                n.row = sg.g.row;
+                n.head = sg.head;
+                n.rows = kGroup * sg.g.nrows;
+            }
+            reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = n;
+        }
       } else if (warp == 2 && !FP8) {
         // ============================================================ V rows without a position
         uint32_t st = 0, ph = 0;
@@ -739,18 +744,31 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t s_ph = 0, oph = 0, qph = 0;
         uint8_t* stg = smem + kPcStage + (warp - 4) * kPcStageBytes;
         const uint32_t stg_s = sbase + kPcStage + (warp - 4) * kPcStageBytes;
-        // The next pair this tile takes part in.
-        auto fetch = [&]() -> bool {
+        // The next pair this tile takes part in, in few registers (the softmax
+        // needs them): its first chunk's start, chunks, one past its last
+        // position, the tile's first position and packed row; rows, head,
+        // whole and first.
+        struct Work { int ks, n, hi, pos0, row, info; };
+        auto fetch = [&](Work& w) -> bool {
             while (paged_share_next(share, sg, first)) {
+                const bool f = first;
                 first = false;
-                if (t == 0 || sg.g.nrows > kTokPerTile) return true;
+                if (t != 0 && sg.g.nrows <= kTokPerTile) continue;
+                const PcGroup g = pc_group(p, sg.g);
+                w.ks = g.kb + kKeyChunk * sg.t0;
+                w.n = sg.t1 - sg.t0;
+                w.hi = g.hi;
+                w.pos0 = g.p0 + kTokPerTile * t;
+                w.row = g.row + kTokPerTile * t;
+                w.info = (sg.g.nrows - kTokPerTile * t) << 8 | sg.head << 2 | (sg.whole ? 2 : 0) | (f ? 1 : 0);
+                return true;
             }
             return false;
         };
         // Query prologue: thread r normalises row r of the tile in place
         // (weight-form RMSNorm), rotates channel pairs (f, f + 64) by pos x
         // theta^(-f/64) and leaves FP16 x 2^eq.
-        auto prepare_q = [&](const PcGroup& gr) -> bool {
+        auto prepare_q = [&](const int pos0) -> bool {
             if (!__all_sync(0xffffffffu, mbar_wait(bar(PC_Q_FULL + t), qph, abort_flag, status))) return false;
             qph ^= 1;
             const uint8_t* tab = stg + (lane >> 3) * kPcTabStride;
@@ -759,7 +777,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 // once lane 0's earlier output stores have read it
                 if (lane == 0) bulk_wait_group_read0();
                 __syncwarp();
-                const int pos = gr.p0 + kTokPerTile * t + tl;
+                const int pos = pos0 + tl;
                 const double* inv = reinterpret_cast<const double*>(p.ws + L.inv);
                 uint8_t* tw = stg + (lane >> 3) * kPcTabStride;
 #pragma unroll
@@ -828,24 +846,18 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_arrive(bar(PC_Q_READY + t));
             return true;
         };
-        bool have = fetch();
-        PcGroup gr = {};
-        if (have) {
-            gr = pc_group(p, sg.g);
-            have = prepare_q(gr);
-        }
+        Work wk = {};
+        bool have = fetch(wk);
+        if (have) have = prepare_q(wk.pos0);
         while (have) {
-            const PagedSeg cur = sg;
-            const int h = kGroup * cur.head + hl;
-            const int pos = gr.p0 + kTokPerTile * t + tl;            // this row's position
-            const int pos0 = gr.p0 + kTokPerTile * t;                // the tile's first
+            const int pos0 = wk.pos0, pos = pos0 + tl;               // the tile's first position, this row's
             const int wlo = p.window > 0 ? pos - p.window + 1 : -(1 << 30);
             float m = -INFINITY, l = 0.f;                            // the sink joins at the end
             bool alive = true;
-            for (int ch = cur.t0; ch < cur.t1; ++ch) {
-                const bool first_ch = ch == cur.t0;
-                const int ks = gr.kb + kKeyChunk * ch;
-                const int nc = pc_cols(ks, gr.hi);
+            for (int ch = 0; ch < wk.n; ++ch) {
+                const bool first_ch = ch == 0;
+                const int ks = wk.ks + kKeyChunk * ch;
+                const int nc = pc_cols(ks, wk.hi);
                 const int nblk = (nc + 31) >> 5;
                 if (!__all_sync(0xffffffffu, mbar_wait(bar(PC_S_FULL + t), s_ph, abort_flag, status))) { alive = false; break; }
                 s_ph ^= 1;
@@ -992,23 +1004,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!alive) break;
 
             // ---- the next pair's queries, under this one's last products
-            const PcGroup gc = gr;
-            have = fetch();
-            if (have) {
-                gr = pc_group(p, sg.g);
-                if (!prepare_q(gr)) break;
-            }
+            const int row0 = wk.row, info = wk.info;
+            const int nrows = info >> 8, head = info >> 2 & 63;      // of this tile
+            have = fetch(wk);
+            if (have && !prepare_q(wk.pos0)) break;
 
             // ---- epilogue
             if (!__all_sync(0xffffffffu, mbar_wait(bar(PC_O_FULL + t), oph, abort_flag, status))) break;
             oph ^= 1;
             tc_fence_after();
-            if (!cur.whole) {
+            if (!(info & 2)) {
                 // partial: m, l and O in FP32, channel quads outermost so that
                 // the rows of a warp are consecutive
                 tc_fence_before();
-                if (kTokPerTile * t + 4 * (warp & 3) >= cur.g.nrows) continue;    // none of the warp's rows is a new token's
-                float* dst = reinterpret_cast<float*>(p.ws + L.cpart) + (2 * (size_t)blockIdx.x + (cur.first ? 0 : 1)) * kChunkPart;
+                if (4 * (warp & 3) >= nrows) continue;    // none of the warp's rows is a new token's
+                float* dst = reinterpret_cast<float*>(p.ws + L.cpart) + (2 * (size_t)blockIdx.x + (info & 1 ? 0 : 1)) * kChunkPart;
                 const int row = 128 * t + r;
                 dst[row] = m;
                 dst[256 + row] = l;
@@ -1027,11 +1037,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 continue;
             }
             float lse, scale;
+            const int h = kGroup * head + hl;
             paged_finish(m, l, p.sinks[h], &scale, &lse);
             // Valid tokens of this warp's 4: rows behind the sequence's last
             // new token are other sequences' or nobody's
-            const int wt0 = kTokPerTile * t + 4 * (warp & 3);
-            const int nvw = max(0, min(4, cur.g.nrows - wt0));
+            const int wt0 = 4 * (warp & 3);
+            const int nvw = max(0, min(4, nrows - wt0));
             const int sw = lane & 7;
 #pragma unroll 1
             for (int hb = 0; hb < 2; ++hb) {
@@ -1056,16 +1067,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 __syncwarp();
                 if (lane == 0 && nvw > 0) {
                     if (nvw == 4) {
-                        tma_store_3d(&tm_o, stg_s, 64 * hb, kGroup * cur.head, gc.row + wt0);
+                        tma_store_3d(&tm_o, stg_s, 64 * hb, kGroup * head, row0 + wt0);
                     } else {
                         for (int k = 0; k < nvw; ++k)
-                            tma_store_3d(&tm_o1, stg_s + 1024u * k, 64 * hb, kGroup * cur.head, gc.row + wt0 + k);
+                            tma_store_3d(&tm_o1, stg_s + 1024u * k, 64 * hb, kGroup * head, row0 + wt0 + k);
                     }
                     bulk_commit_group();
                 }
             }
-            if (kTokPerTile * t + tl < cur.g.nrows && p.lse)
-                p.lse[(size_t)h * c.T + gc.row + kTokPerTile * t + tl] = lse;
+            if (tl < nrows && p.lse) p.lse[(size_t)h * c.T + row0 + tl] = lse;
             tc_fence_before();
         }
     }
@@ -1081,56 +1091,58 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// Folds the partials of the pairs that several CTAs hold (in CTA order).
-// Block (x, y): the pair that CTA x + 1's share begins inside of, if x + 1 is
-// the first CTA to do so; rows 32 y .. 32 y + 31 (a lane a row, a warp eight
-// channel quads).
+// Folds the partials of the pairs that several CTAs hold (in CTA order): block
+// (x, y) what CTA x + 1's note says, rows 32 y .. 32 y + 31 (a lane a row, a
+// warp eight channel quads).
 __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedAttnParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const PagedCache& c = p.c;
-    const int ng = c.ng, nh = kGroup * ng;
+    const int nh = kGroup * c.ng;
     const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
-    const PagedPlanHeader* hdr = reinterpret_cast<const PagedPlanHeader*>(p.ws + L.header);
     const float* part = reinterpret_cast<const float*>(p.ws + L.cpart);
     griddep_wait();
-    PagedShare s;
-    const long long* prefix = reinterpret_cast<const long long*>(p.ws + L.prefix);
-    if (!paged_share_begin(s, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.groups), prefix, ng,
-                           blockIdx.x + 1, p.chunk_ctas))
-        return;
-    PagedSeg sg;
-    if (!paged_share_next(s, sg, true) || sg.t0 == 0) return;   // the share begins with a pair
-    const long long W = hdr->chunk.tiles * ng, G = W < (long long)p.chunk_ctas ? W : (long long)p.chunk_ctas;
-    const PagedParts pp = paged_parts(W, G, W * ((long long)blockIdx.x + 1) / G - sg.t0, sg.g.tiles);
-    if (pp.cf != (int)blockIdx.x) return;                       // an earlier block folds this pair
-    const int row = 32 * blockIdx.y + lane, tok = row >> 3;
-    if (4 * (int)blockIdx.y >= sg.g.nrows) return;
-    float M = -INFINITY;
-    for (int x = pp.cf; x <= pp.cl; ++x) M = fmaxf(M, part[pp.slot(x) * kChunkPart + row]);
-    float l = 0.f;
+    const PagedNote n = reinterpret_cast<const PagedNote*>(p.ws + L.notes)[blockIdx.x + 1];
+    const int row = 32 * blockIdx.y + lane;
+    if (!n.fold || 32 * (int)blockIdx.y >= n.rows) return;
+    const PagedParts pp = n.parts;
+    // two parts a round (most pairs have two), their loads all on their way
+    // at once; the running max of a later round rescales what is there
+    float M = -INFINITY, l = 0.f;
     float4 o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x = pp.cf; x <= pp.cl; ++x) {
-        const float* b = part + pp.slot(x) * kChunkPart;
-        const float mx = b[row], lx = b[256 + row];
-        const float a = mx > -INFINITY ? exp2f(mx - M) : 0.f;
-        const float4* o4 = reinterpret_cast<const float4*>(b + 512) + (size_t)(8 * warp) * 256 + row;
-        l += lx * a;
+    for (int x = pp.cf; x <= pp.cl; x += 2) {
+        const bool two = x + 1 <= pp.cl;
+        const float* b0 = part + pp.slot(x) * kChunkPart;
+        const float* b1 = two ? part + pp.slot(x + 1) * kChunkPart : b0;
+        const float m0 = __ldcg(b0 + row), m1 = two ? __ldcg(b1 + row) : -INFINITY;
+        const float l0 = __ldcg(b0 + 256 + row), l1 = two ? __ldcg(b1 + 256 + row) : 0.f;
+        const float4* p0 = reinterpret_cast<const float4*>(b0 + 512) + (size_t)(8 * warp) * 256 + row;
+        const float4* p1 = reinterpret_cast<const float4*>(b1 + 512) + (size_t)(8 * warp) * 256 + row;
+        float4 v0[8], v1[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float4 v = o4[(size_t)j * 256];
-            o[j].x += v.x * a;
-            o[j].y += v.y * a;
-            o[j].z += v.z * a;
-            o[j].w += v.w * a;
+            v0[j] = __ldcg(p0 + (size_t)j * 256);
+            v1[j] = __ldcg(p1 + (size_t)j * 256);
+        }
+        const float Mn = fmaxf(M, fmaxf(m0, m1));
+        const float ab = M > -INFINITY ? exp2f(M - Mn) : 0.f;
+        const float a0 = m0 > -INFINITY ? exp2f(m0 - Mn) : 0.f, a1 = m1 > -INFINITY ? exp2f(m1 - Mn) : 0.f;
+        M = Mn;
+        l = l * ab + l0 * a0 + l1 * a1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            o[j].x = o[j].x * ab + v0[j].x * a0 + v1[j].x * a1;
+            o[j].y = o[j].y * ab + v0[j].y * a0 + v1[j].y * a1;
+            o[j].z = o[j].z * ab + v0[j].z * a0 + v1[j].z * a1;
+            o[j].w = o[j].w * ab + v0[j].w * a0 + v1[j].w * a1;
         }
     }
-    if (tok >= sg.g.nrows) return;
-    const int h = kGroup * sg.head + (row & 7);
+    if (row >= n.rows) return;
+    const int h = kGroup * n.head + (row & 7);
     float scale, lse;
     paged_finish(M, l, p.sinks[h], &scale, &lse);
-    const size_t t = (size_t)(sg.g.row + tok);
+    const size_t t = (size_t)(n.row + (row >> 3));
     uint4* dst = reinterpret_cast<uint4*>(p.out + (t * nh + h) * kHD + 32 * warp);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -1176,8 +1188,8 @@ cudaError_t launch_chunk(const CUtensorMap* m, const PagedAttnParams& p, cudaStr
     cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
     if (SRC == kPcStaged) {
-        // a warp a block of 16 positions, at most eight blocks an SM
-        const int n = (p.stage_rows / 16 + kExpandThreads / 32 - 1) / (kExpandThreads / 32);
+        // a warp for 16 positions of a head, at most eight blocks an SM
+        const int n = (p.c.B * (p.stage_rows / 16) * p.c.ng + kExpandThreads / 32 - 1) / (kExpandThreads / 32);
         cfg.gridDim = dim3(n < 8 * p.chunk_ctas ? n : 8 * p.chunk_ctas);
         cfg.blockDim = dim3(kExpandThreads);
         e = cudaLaunchKernelEx(&cfg, paged_expand_kernel, p);
@@ -1209,8 +1221,8 @@ flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s) {
     const CUtensorMapDataType f16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if (p.stage_rows > 0) {
         const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
-        if (st == FLINT_OK) st = pc_map(enc, &m[1], f16, p.ws + L.stage_k, p.stage_rows, c.ng, kKeyChunk, 1);
-        if (st == FLINT_OK) st = pc_map(enc, &m[2], bf, p.ws + L.stage_v, p.stage_rows, c.ng, kKeyChunk, 1);
+        if (st == FLINT_OK) st = pc_map(enc, &m[1], f16, p.ws + L.stage_k, (cuuint64_t)c.B * p.stage_rows, c.ng, kKeyChunk, 1);
+        if (st == FLINT_OK) st = pc_map(enc, &m[2], bf, p.ws + L.stage_v, (cuuint64_t)c.B * p.stage_rows, c.ng, kKeyChunk, 1);
     } else if (!fp8) {
         if (st == FLINT_OK) st = pc_map(enc, &m[1], f16, p.k_pages, ps, rows, (cuuint32_t)ps, 1);
         if (st == FLINT_OK) st = pc_map(enc, &m[2], bf, p.v_pages, ps, rows, (cuuint32_t)ps, 1);

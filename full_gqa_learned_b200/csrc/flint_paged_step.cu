@@ -286,7 +286,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     const int ng = c.ng, nh = kGroup * ng;
     const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, 0, 0);
     float* part = reinterpret_cast<float*>(p.ws + L.spart);
-    StepNote* note = reinterpret_cast<StepNote*>(p.ws + L.notes) + blockIdx.x;
+    PagedNote* note = reinterpret_cast<PagedNote*>(p.ws + L.notes) + blockIdx.x;
     float* s_m = reinterpret_cast<float*>(smem + S::ml);
     float* s_l = s_m + kStepWarps * S::rows;
     float* s_fin = reinterpret_cast<float*>(smem + S::fin);
@@ -303,7 +303,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     bool bad;
     const bool work = step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad);
     if (!work) {
-        if (tid == 0) *note = StepNote{bad ? kStatusInvalid : kStatusOk};
+        if (tid == 0) *note = PagedNote{bad ? kStatusInvalid : kStatusOk};
         return;
     }
     if (tid == 0) {
@@ -442,7 +442,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         if (first && tid == 0) {
             // a pair that the share begins inside of is held in part by the
             // CTAs before, too: the first CTA of those leaves the fold a note
-            StepNote n = {};
+            PagedNote n = {};
             if (sg.t0 > 0) {
                 n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.tiles);
                 n.fold = n.parts.cf == (int)blockIdx.x - 1;
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kFoldThreads, 2) paged_fold_kernel(const Paged
     const PagedCache& c = p.c;
     const int nh = kGroup * c.ng;
     const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, 0, 0);
-    const StepNote* notes = reinterpret_cast<const StepNote*>(p.ws + L.notes);
+    const PagedNote* notes = reinterpret_cast<const PagedNote*>(p.ws + L.notes);
     const float* part = reinterpret_cast<const float*>(p.ws + L.spart);
     griddep_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kFoldThreads, 2) paged_fold_kernel(const Paged
         if (tid == 0) *reinterpret_cast<int*>(p.ws + L.header) = timeout ? kStatusTimeout : invalid ? kStatusInvalid : kStatusOk;
     }
     if ((int)blockIdx.x + 1 >= p.step_ctas) return;
-    const StepNote n = notes[blockIdx.x + 1];
+    const PagedNote n = notes[blockIdx.x + 1];
     const int r = (kFoldThreads / 32) * blockIdx.y + warp;    // the warp's row
     if (!n.fold || r >= n.rows) return;
     const PagedParts pp = n.parts;
@@ -948,15 +948,15 @@ constexpr int kPagedMaxSms = 148;
 // kernel, others the chunk kernel.
 constexpr int kStepMaxNew = 8;
 
-// Positions that the chunk kernel's calls on 8-bit pages have expanded to 16
-// bits at most: each sequence's window of its new tokens, from a page's start.
-constexpr size_t kStageMost = (size_t)512 << 20;
-int stage_rows(int B, int T, int max_new, int max_pages, int page_size, int ng, int window) {
+// Positions a sequence has room for where the chunk kernel's calls on 8-bit
+// pages expand them to 16 bits: the window of its new tokens, from a page's
+// start; 0 where all sequences' would take more than 512 MiB.
+int stage_rows(int B, int max_new, int max_pages, int page_size, int ng, int window) {
     long long span = (long long)max_pages * page_size;
     if (span > FLINT_MAX_TOKENS) span = FLINT_MAX_TOKENS;
     if (window > 0 && span > (long long)window + max_new + page_size) span = (long long)window + max_new + page_size;
-    const long long rows = (span + 15) / 16 * 16 * (B < T ? B : T);
-    return rows * ng * kHD * 4 <= (long long)kStageMost ? (int)rows : 0;
+    span = (span + 15) / 16 * 16;
+    return span * B * ng * kHD * 4 <= 512LL << 20 ? (int)span : 0;
 }
 
 }  // namespace
@@ -964,7 +964,7 @@ int stage_rows(int B, int T, int max_new, int max_pages, int page_size, int ng, 
 size_t paged_attn_workspace(int B, int T, int max_new, int max_pages, int page_size, int ng, int window, bool fp8) {
     const bool chunk = max_new > kStepMaxNew;
     return paged_ws(B, T, ng, kPagedMaxSms * kStepCtasPerSm, chunk ? kPagedMaxSms : 0,
-                    chunk && fp8 ? stage_rows(B, T, max_new, max_pages, page_size, ng, window) : 0).total;
+                    chunk && fp8 ? stage_rows(B, max_new, max_pages, page_size, ng, window) : 0).total;
 }
 
 flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c, int sms, size_t workspace_bytes,
@@ -977,7 +977,7 @@ flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c,
     p.stage_rows = 0;
     if (p.chunk_ctas) {
         // 8-bit pages: expanded first where the caller gave room for it
-        const int rows = fp8 ? stage_rows(c.B, c.T, p.max_new, c.max_pages, 1 << c.ps_log2, c.ng, p.window) : 0;
+        const int rows = fp8 ? stage_rows(c.B, p.max_new, c.max_pages, 1 << c.ps_log2, c.ng, p.window) : 0;
         if (rows && paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, rows).total <= workspace_bytes) p.stage_rows = rows;
         return launch_paged_chunk(p, s);
     }
