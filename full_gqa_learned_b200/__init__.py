@@ -256,52 +256,65 @@ def paged_workspace_bytes(B: int, T: int, max_new: int, max_pages: int, page_siz
                                                                int(bool(eight_bit))))
 
 
-def _check_on(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+def _check_as(t, name, dtype, shape, dev):
+    """_check, and that t is on dev; one short test where all is well (a
+    decode step's calls are a few microseconds of GPU work)."""
+    if t.__class__.__name__ == "Tensor" and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
+    _check(t, name, dtype, shape)
+    if t.device != dev:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
 
 
 def _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu):
-    """Checks what the paged calls take alike; returns (B, kv_heads, page size)."""
+    """Checks what the paged calls take alike; returns (device, B, kv_heads, page size)."""
     import torch
     if (k_scales is None) != (v_scales is None):
         raise ValueError("give k_scales and v_scales (8-bit pages) or neither (16-bit pages)")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.shape[3] != HEAD_DIM:
         raise ValueError("k_pages must be [num_pages, kv_heads, page_size, 128]")
-    shape = tuple(k_pages.shape)
+    shape, dev = k_pages.shape, k_pages.device
     if k_scales is None:
-        _check(k_pages, "k_pages", torch.float16)
-        _check(v_pages, "v_pages", torch.bfloat16, shape)
+        _check_as(k_pages, "k_pages", torch.float16, shape, dev)
+        _check_as(v_pages, "v_pages", torch.bfloat16, shape, dev)
     else:
-        _check(k_pages, "k_pages", torch.float8_e4m3fn)
-        _check(v_pages, "v_pages", torch.float8_e4m3fn, shape)
-        _check(k_scales, "k_scales", torch.float8_e8m0fnu, shape[:3])
-        _check(v_scales, "v_scales", torch.float8_e8m0fnu, shape[:3])
-    _check(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2:
+        _check_as(k_pages, "k_pages", torch.float8_e4m3fn, shape, dev)
+        _check_as(v_pages, "v_pages", torch.float8_e4m3fn, shape, dev)
+        _check_as(k_scales, "k_scales", torch.float8_e8m0fnu, shape[:3], dev)
+        _check_as(v_scales, "v_scales", torch.float8_e8m0fnu, shape[:3], dev)
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B = int(page_table.shape[0])
-    _check(start, "cache_len", torch.int32, (B,))
-    _check(cu, "cu_new", torch.int32, (B + 1,))
-    _check_on(k_pages.device, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales, page_table=page_table,
-              cache_len=start, cu_new=cu)
-    return B, shape[1], shape[2]
+    B = page_table.shape[0]
+    _check_as(page_table, "page_table", torch.int32, page_table.shape, dev)
+    _check_as(start, "cache_len", torch.int32, (B,), dev)
+    _check_as(cu, "cu_new", torch.int32, (B + 1,), dev)
+    return dev, B, shape[1], shape[2]
 
 
-def _paged_stream(stream, dev, allocated):
-    """The call's stream as a number.  Tensors that the call allocated on
-    torch's current stream are kept until another stream has passed them."""
+def _paged_call(fn, args, workspace, dev, stream, own):
+    """Runs fn(*args, workspace, its bytes, stream) on dev.  Tensors that the
+    call allocated on torch's current stream (own) are kept until another
+    stream has passed them."""
     import torch
+    if workspace.__class__ is not torch.Tensor or workspace.dtype is not torch.uint8:
+        _check(workspace, "workspace", torch.uint8)
     current = torch.cuda.current_stream(dev)
-    if stream is None:
-        return current.cuda_stream
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    if stream.cuda_stream != current.cuda_stream:
-        for t in allocated:
-            t.record_stream(stream)
-    return stream.cuda_stream
+    ptr = current.cuda_stream
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        if stream.cuda_stream != ptr:
+            ptr = stream.cuda_stream
+            for t in own:
+                t.record_stream(stream)
+    args += (workspace.data_ptr(), workspace.numel(), ptr)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != 0:
+        raise FlintError(st, load_library().flint_attn_last_error().decode())
 
 
 def paged_append(k, v, k_norm_w, k_pages, v_pages, page_table, cache_len, cu_new, *, k_scales=None,
@@ -320,28 +333,21 @@ def paged_append(k, v, k_norm_w, k_pages, v_pages, page_table, cache_len, cu_new
     [P,g,ps] float8_e8m0fnu.
     """
     import torch
-    lib = load_library()
-    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
-    dev = k_pages.device
-    T = int(k.shape[0]) if k.dim() >= 1 else 0
-    _check(k, "k", torch.bfloat16, (T, g, HEAD_DIM))
-    _check(v, "v", torch.bfloat16, (T, g, HEAD_DIM))
-    _check(k_norm_w, "k_norm_w", torch.float32, (HEAD_DIM,))
-    _check_on(dev, k=k, v=v, k_norm_w=k_norm_w)
+    lib = _lib or load_library()
+    dev, B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
+    T = k.shape[0] if k.dim() >= 1 else 0
+    _check_as(k, "k", torch.bfloat16, (T, g, HEAD_DIM), dev)
+    _check_as(v, "v", torch.bfloat16, (T, g, HEAD_DIM), dev)
+    _check_as(k_norm_w, "k_norm_w", torch.float32, (HEAD_DIM,), dev)
     own = []
     if workspace is None:
         workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
         own.append(workspace)
-    _check(workspace, "workspace", torch.uint8)
-    _check_on(dev, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.flint_paged_append(
-            _ptr(k), _ptr(v), _ptr(k_norm_w), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-            _ptr(page_table), _ptr(cache_len), _ptr(cu_new), B, T, int(page_table.shape[1]),
-            int(k_pages.shape[0]), ps, g, int(bool(use_rope)), float(rope_theta), float(eps),
-            _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
-    if st != 0:
-        raise FlintError(st, lib.flint_attn_last_error().decode())
+    _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _paged_call(lib.flint_paged_append, (
+        k.data_ptr(), v.data_ptr(), k_norm_w.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+        _ptr(v_scales), page_table.data_ptr(), cache_len.data_ptr(), cu_new.data_ptr(), B, T, page_table.shape[1],
+        k_pages.shape[0], ps, g, int(bool(use_rope)), float(rope_theta), float(eps)), workspace, dev, stream, own)
     paged_append.last_workspace = workspace
 
 
@@ -354,9 +360,8 @@ def paged_read(k_pages, v_pages, page_table, start, cu_out, T: int, *, k_scales=
     they were (unset unless k and v are given).  Other arguments as for
     paged_append."""
     import torch
-    lib = load_library()
-    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu_out)
-    dev = k_pages.device
+    lib = _lib or load_library()
+    dev, B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu_out)
     T = int(T)
     if T < 0:
         raise ValueError("T must not be negative")
@@ -370,17 +375,13 @@ def paged_read(k_pages, v_pages, page_table, start, cu_out, T: int, *, k_scales=
     if workspace is None:
         workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
         own.append(workspace)
-    _check(k, "k", torch.float16, (T, g, HEAD_DIM))
-    _check(v, "v", torch.bfloat16, (T, g, HEAD_DIM))
-    _check(workspace, "workspace", torch.uint8)
-    _check_on(dev, k=k, v=v, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.flint_paged_read(
-            _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(start),
-            _ptr(cu_out), B, T, int(page_table.shape[1]), int(k_pages.shape[0]), ps, g, _ptr(k), _ptr(v),
-            _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
-    if st != 0:
-        raise FlintError(st, lib.flint_attn_last_error().decode())
+    _check_as(k, "k", torch.float16, (T, g, HEAD_DIM), dev)
+    _check_as(v, "v", torch.bfloat16, (T, g, HEAD_DIM), dev)
+    _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _paged_call(lib.flint_paged_read, (
+        k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(),
+        start.data_ptr(), cu_out.data_ptr(), B, T, page_table.shape[1], k_pages.shape[0], ps, g, k.data_ptr(),
+        v.data_ptr()), workspace, dev, stream, own)
     paged_read.last_workspace = workspace
     return k, v
 
@@ -401,38 +402,36 @@ def attn_paged(q, q_norm_w, sinks, k_pages, v_pages, page_table, cache_len, cu_n
     unless out and lse are given).  Other arguments as for paged_append.
     """
     import torch
-    lib = load_library()
-    B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
-    dev = k_pages.device
-    T = int(q.shape[0]) if q.dim() >= 1 else 0
+    lib = _lib or load_library()
+    dev, B, g, ps = _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, cache_len, cu_new)
+    T = q.shape[0] if q.dim() >= 1 else 0
     nh = HQ // HKV * g
-    _check(q, "q", torch.bfloat16, (T, nh, HEAD_DIM))
-    _check(q_norm_w, "q_norm_w", torch.float32, (HEAD_DIM,))
-    _check(sinks, "sinks", torch.float32, (nh,))
+    _check_as(q, "q", torch.bfloat16, (T, nh, HEAD_DIM), dev)
+    _check_as(q_norm_w, "q_norm_w", torch.float32, (HEAD_DIM,), dev)
+    _check_as(sinks, "sinks", torch.float32, (nh,), dev)
+    max_new, window, width = int(max_new), int(window), page_table.shape[1]
     own = []
     if out is None:
         out = torch.empty((T, nh * HEAD_DIM), dtype=torch.bfloat16, device=dev)
         own.append(out)
+    else:
+        _check_as(out, "out", torch.bfloat16, (T, nh * HEAD_DIM), dev)
     if lse is None and want_lse:
         lse = torch.empty((nh, T), dtype=torch.float32, device=dev)
         own.append(lse)
+    elif lse is not None:
+        _check_as(lse, "lse", torch.float32, (nh, T), dev)
     if workspace is None:
-        workspace = torch.empty(max(256, paged_workspace_bytes(
-            B, T, max_new, int(page_table.shape[1]), ps, kv_heads=g, window=window, eight_bit=k_scales is not None)), dtype=torch.uint8, device=dev)
+        need = lib.flint_attn_paged_workspace_bytes(B, T, max_new, width, ps, g, window, k_scales is not None)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
         own.append(workspace)
-    _check(out, "out", torch.bfloat16, (T, nh * HEAD_DIM))
-    if lse is not None:
-        _check(lse, "lse", torch.float32, (nh, T))
-    _check(workspace, "workspace", torch.uint8)
-    _check_on(dev, q=q, q_norm_w=q_norm_w, sinks=sinks, out=out, lse=lse, workspace=workspace)
-    with torch.cuda.device(dev):
-        st = lib.flint_attn_paged(
-            _ptr(q), _ptr(q_norm_w), _ptr(sinks), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
-            _ptr(page_table), _ptr(cache_len), _ptr(cu_new), B, T, int(max_new), int(page_table.shape[1]),
-            int(k_pages.shape[0]), ps, g, int(window), int(bool(use_rope)), float(rope_theta), float(eps),
-            _ptr(out), _ptr(lse), _ptr(workspace), int(workspace.numel()), _paged_stream(stream, dev, own))
-    if st != 0:
-        raise FlintError(st, lib.flint_attn_last_error().decode())
+    else:
+        _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _paged_call(lib.flint_attn_paged, (
+        q.data_ptr(), q_norm_w.data_ptr(), sinks.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+        _ptr(v_scales), page_table.data_ptr(), cache_len.data_ptr(), cu_new.data_ptr(), B, T, max_new, width,
+        k_pages.shape[0], ps, g, window, int(bool(use_rope)), float(rope_theta), float(eps), out.data_ptr(),
+        _ptr(lse)), workspace, dev, stream, own)
     attn_paged.last_workspace = workspace
     return out, lse
 
