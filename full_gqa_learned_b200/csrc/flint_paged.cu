@@ -61,19 +61,38 @@ __device__ void paged_check_block(const PagedCache& c, int* status, bool keep_no
     if (threadIdx.x == 0) *status = s_bad ? kStatusInvalid : kStatusOk;
 }
 
-// Sequence, position and pool row of packed row t (warp-uniform t); false
-// where the row belongs to no sequence or has no page.
-__device__ __forceinline__ bool paged_locate(const PagedCache& c, int t, int* pos, int* page, int* slot) {
-    const int b = warp_last_leq(c.cu, c.B, t);
-    const int a = c.cu[b], z = c.cu[b + 1], L = c.len[b];
-    if (t < a || t >= z || L < 0) return false;
+// Places of the warp's tokens t0 .. t0 + n - 1 (n <= 32): lane i holds token
+// t0 + i's position and page, page -1 where it has none or belongs to nobody
+// (`own`: it belongs to a sequence's run).  One search a warp; lanes walk on
+// from there.
+struct PagedPlace { int pos, page; bool own; };
+__device__ __forceinline__ PagedPlace paged_locate(const PagedCache& c, int t0, int n) {
+    const int t = t0 + (threadIdx.x & 31);
+    PagedPlace r = {0, -1, false};
+    int b = warp_last_leq(c.cu, c.B, t0);
+    if ((int)(threadIdx.x & 31) >= n || t >= c.T) return r;
+    int a = __ldg(c.cu + b), z = __ldg(c.cu + b + 1);
+    while (t >= z && b + 1 < c.B) {
+        a = z;
+        z = __ldg(c.cu + ++b + 1);
+    }
+    const int L = __ldg(c.len + b);
+    r.own = t < __ldg(c.cu + c.B);
+    if (t < a || t >= z || L < 0) return r;
     const long long p = (long long)L + (t - a);
-    if (p >= FLINT_MAX_TOKENS || (p >> c.ps_log2) >= c.max_pages) return false;
-    *pos = (int)p;
-    *slot = (int)p & ((1 << c.ps_log2) - 1);
-    *page = c.table[(size_t)b * c.max_pages + (int)(p >> c.ps_log2)];
-    return *page >= 0 && *page < c.num_pages;
+    if (p >= FLINT_MAX_TOKENS || (p >> c.ps_log2) >= c.max_pages) return r;
+    r.pos = (int)p;
+    const int page = __ldg(c.table + (size_t)b * c.max_pages + (int)(p >> c.ps_log2));
+    r.page = page < c.num_pages ? max(page, -1) : -1;
+    return r;
 }
+
+// Tokens a warp takes: eight on long calls, so that one look-up serves many
+// rows and many loads are on their way; fewer where a call of few tokens would
+// leave SMs idle.  Measured (launch included): reading 103,592 tokens of 8-bit
+// pages 88 us with one token a warp, 76 with eight; appending 21,455 is the
+// same 20 us either way.
+__host__ __device__ inline int paged_tokens_per_warp(int T) { return T >= 16384 ? 8 : T >= 4096 ? 4 : T >= 2048 ? 2 : 1; }
 
 // E8M0 exponent e of a row whose largest magnitude is a.
 __device__ __forceinline__ int paged_exponent(float a) {
@@ -125,28 +144,23 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
         w0[e] = p.k_norm_w[8 * sub + e];
         w1[e] = p.k_norm_w[64 + 8 * sub + e];
     }
-    const int nrows = p.c.T * NG;                             // T <= 2^24
-    const int nw = (gridDim.x - 1) * (kPagedThreads >> 5);
-    for (int wi = blockIdx.x * (kPagedThreads >> 5) + warp; 4 * wi < nrows; wi += nw) {
-        const int r = 4 * wi + grp;
-        const bool in = r < nrows;
-        const size_t src = (size_t)(in ? r : 0) * kHD;
+    // a pass: 4 / NG tokens, four rows of eight lanes
+    constexpr int kTok = 4 / NG;
+    const int per = max(kTok, paged_tokens_per_warp(p.c.T));
+    const long long t0 = (long long)(blockIdx.x * (kPagedThreads >> 5) + warp) * per;
+    if (t0 < p.c.T) {
+      const PagedPlace place = paged_locate(p.c, (int)t0, per);
+#pragma unroll 2
+      for (int i = 0; i < per; i += kTok) {
+        const int tok = i + grp / NG, head = grp % NG;
+        const bool in = t0 + tok < p.c.T;
+        const size_t src = ((size_t)(in ? t0 + tok : t0) * NG + head) * kHD;
         const uint4 ka = *reinterpret_cast<const uint4*>(p.k + src + 8 * sub);
         const uint4 kb = *reinterpret_cast<const uint4*>(p.k + src + 64 + 8 * sub);
         const uint4 va = *reinterpret_cast<const uint4*>(p.v + src + 8 * sub);
         const uint4 vb = *reinterpret_cast<const uint4*>(p.v + src + 64 + 8 * sub);
-        // the warp's 4 / NG tokens, one search each
-        int pos = 0, page = 0, slot = 0;
-        bool ok = false;
-#pragma unroll
-        for (int i = 0; i < 4 / NG; ++i) {
-            const int t = (4 * wi) / NG + i;
-            int po = 0, pg = 0, sl = 0;
-            bool o = false;
-            if (t < p.c.T) o = paged_locate(p.c, t, &po, &pg, &sl);
-            if (grp / NG == i) { pos = po; page = pg; slot = sl; ok = o; }
-        }
-        ok = ok && in;
+        const int pos = __shfl_sync(0xffffffffu, place.pos, tok), page = __shfl_sync(0xffffffffu, place.page, tok);
+        const bool ok = in && page >= 0;
         float x0[8], x1[8];
         const uint32_t aw[4] = {ka.x, ka.y, ka.z, ka.w}, bw[4] = {kb.x, kb.y, kb.z, kb.w};
         float ss = 0.f;
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
                 x1[e] = y1;
             }
         }
-        const size_t row = ok ? paged_row(p.c, page, r % NG, slot) : 0;
+        const size_t row = ok ? paged_row(p.c, page, head, pos & ((1 << p.c.ps_log2) - 1)) : 0;
         if constexpr (!FP8) {
             if (ok) {
                 __half2 h[8];
@@ -234,6 +248,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
                 }
             }
         }
+      }
     }
 }
 
@@ -261,57 +276,66 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadPar
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int grp = lane >> 3, sub = lane & 7;
-    const int nrows = p.c.T * NG;
-    const int nw = (gridDim.x - 1) * (kPagedThreads >> 5);
-    for (int wi = blockIdx.x * (kPagedThreads >> 5) + warp; 4 * wi < nrows; wi += nw) {
-        const int r = 4 * wi + grp;
-        int page = 0, slot = 0;
-        bool ok = false, mine = false;
+    constexpr int kTok = 4 / NG;
+    const int per = max(kTok, paged_tokens_per_warp(p.c.T));
+    const long long t0 = (long long)(blockIdx.x * (kPagedThreads >> 5) + warp) * per;
+    if (t0 < p.c.T) {
+      const PagedPlace place = paged_locate(p.c, (int)t0, per);
+      // four passes' loads on their way at once
+      for (int i0 = 0; i0 < per; i0 += 4 * kTok) {
+        uint4 ka[4], kb[4], va[4], vb[4];
+        uint32_t sk[4], sv[4];
+        bool mine[4];
 #pragma unroll
-        for (int i = 0; i < 4 / NG; ++i) {
-            const int t = (4 * wi) / NG + i;
-            int po = 0, pg = 0, sl = 0;
-            bool o = false;
-            if (t < p.c.T) o = paged_locate(p.c, t, &po, &pg, &sl);
-            if (grp / NG == i) { page = pg; slot = sl; ok = o; mine = t < p.c.cu[p.c.B]; }
-        }
-        if (r >= nrows || !mine) continue;                    // rows behind the last sequence stay as they were
-        const size_t row = ok ? paged_row(p.c, page, r % NG, slot) : 0;
-        uint4 k0 = make_uint4(0, 0, 0, 0), k1 = k0, v0 = k0, v1 = k0;   // a row without a page reads as zeros
-        if constexpr (!FP8) {
-            if (ok) {
+        for (int y = 0; y < 4; ++y) {
+            const int tok = (i0 + y * kTok + grp / NG) & 31;
+            const int pos = __shfl_sync(0xffffffffu, place.pos, tok), page = __shfl_sync(0xffffffffu, place.page, tok);
+            mine[y] = __shfl_sync(0xffffffffu, (int)place.own, tok) != 0 && i0 + y * kTok < per;
+            // a row without a page reads as zeros
+            ka[y] = kb[y] = va[y] = vb[y] = make_uint4(0, 0, 0, 0);
+            sk[y] = sv[y] = 127;
+            if (!mine[y] || page < 0) continue;
+            const size_t row = paged_row(p.c, page, grp % NG, pos & ((1 << p.c.ps_log2) - 1));
+            if constexpr (!FP8) {
                 const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.k_pages) + row * kHD);
                 const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const __half*>(p.v_pages) + row * kHD);
-                k0 = __ldg(ks + sub); k1 = __ldg(ks + 8 + sub);
-                v0 = __ldg(vs + sub); v1 = __ldg(vs + 8 + sub);
+                ka[y] = __ldg(ks + sub); kb[y] = __ldg(ks + 8 + sub);
+                va[y] = __ldg(vs + sub); vb[y] = __ldg(vs + 8 + sub);
+            } else {
+                ka[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + row * kHD) + sub);
+                va[y] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + row * kHD) + sub);
+                sk[y] = __ldg(p.k_scales + row);
+                sv[y] = __ldg(p.v_scales + row);
             }
-            uint4* kd = reinterpret_cast<uint4*>(p.k + (size_t)r * kHD);
-            uint4* vd = reinterpret_cast<uint4*>(p.v + (size_t)r * kHD);
-            kd[sub] = k0; kd[8 + sub] = k1;
-            vd[sub] = v0; vd[8 + sub] = v1;
-        } else {
-            if (ok) {
-                const uint4 kc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) + row * kHD) + sub);
-                const uint4 vc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_pages) + row * kHD) + sub);
-                const float sk = paged_scale(__ldg(p.k_scales + row)), sv = paged_scale(__ldg(p.v_scales + row));
-                const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if (!mine[y]) continue;                           // rows behind the last sequence stay as they were
+            const size_t r = (size_t)(t0 + i0 + y * kTok + grp / NG) * NG + grp % NG;
+            if constexpr (!FP8) {
+                uint4* kd = reinterpret_cast<uint4*>(p.k + r * kHD);
+                uint4* vd = reinterpret_cast<uint4*>(p.v + r * kHD);
+                kd[sub] = ka[y]; kd[8 + sub] = kb[y];
+                vd[sub] = va[y]; vd[8 + sub] = vb[y];
+            } else {
+                const float fk = paged_scale(sk[y]), fv = paged_scale(sv[y]);
+                const uint32_t kw[4] = {ka[y].x, ka[y].y, ka[y].z, ka[y].w}, vw[4] = {va[y].x, va[y].y, va[y].z, va[y].w};
                 __half2 ko[8];
                 __nv_bfloat162 vo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float2 a = paged_decode2(kw[i >> 1] >> (16 * (i & 1)));
                     const float2 b = paged_decode2(vw[i >> 1] >> (16 * (i & 1)));
-                    ko[i] = __floats2half2_rn(a.x * sk, a.y * sk);
-                    vo[i] = __floats2bfloat162_rn(b.x * sv, b.y * sv);
+                    ko[i] = __floats2half2_rn(a.x * fk, a.y * fk);
+                    vo[i] = __floats2bfloat162_rn(b.x * fv, b.y * fv);
                 }
-                k0 = *reinterpret_cast<uint4*>(&ko[0]); k1 = *reinterpret_cast<uint4*>(&ko[4]);
-                v0 = *reinterpret_cast<uint4*>(&vo[0]); v1 = *reinterpret_cast<uint4*>(&vo[4]);
+                uint4* kd = reinterpret_cast<uint4*>(p.k + r * kHD + 16 * sub);
+                uint4* vd = reinterpret_cast<uint4*>(p.v + r * kHD + 16 * sub);
+                kd[0] = *reinterpret_cast<uint4*>(&ko[0]); kd[1] = *reinterpret_cast<uint4*>(&ko[4]);
+                vd[0] = *reinterpret_cast<uint4*>(&vo[0]); vd[1] = *reinterpret_cast<uint4*>(&vo[4]);
             }
-            uint4* kd = reinterpret_cast<uint4*>(p.k + (size_t)r * kHD + 16 * sub);
-            uint4* vd = reinterpret_cast<uint4*>(p.v + (size_t)r * kHD + 16 * sub);
-            kd[0] = k0; kd[1] = k1;
-            vd[0] = v0; vd[1] = v1;
         }
+      }
     }
 }
 
@@ -381,13 +405,13 @@ flint_status_t check_workspace(const void* workspace, size_t have, size_t need) 
     return FLINT_OK;
 }
 
-// Blocks of the row kernels: a warp per four rows, at most eight blocks an SM
-// (they loop over the rest), and the checking block.
-int row_blocks(const PagedCache& c, int sms) {
-    const long long warps = ((long long)c.T * c.ng + 3) / 4;
-    long long n = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
-    if (n > 8LL * sms) n = 8LL * sms;
-    return (int)n + 1;
+// Blocks of the row kernels: a warp per paged_tokens_per_warp tokens (and at
+// least four rows), and the checking block.
+int row_blocks(const PagedCache& c) {
+    int per = paged_tokens_per_warp(c.T);
+    if (per < 4 / c.ng) per = 4 / c.ng;
+    const long long warps = ((long long)c.T + per - 1) / per;
+    return (int)((warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32)) + 1;
 }
 
 template <bool FP8>
@@ -441,7 +465,7 @@ flint_status_t flint_paged_append(const void* k, const void* v, const float* k_n
     p.use_rope = use_rope;
     p.rope_theta = rope_theta;
     p.eps = eps;
-    const int grid = row_blocks(p.c, sms);
+    const int grid = row_blocks(p.c);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (k_scales) launch_append<true>(p, grid, s);
     else launch_append<false>(p, grid, s);
@@ -474,7 +498,7 @@ flint_status_t flint_paged_read(const void* k_pages, const void* v_pages, const 
     p.k = static_cast<__half*>(k);
     p.v = static_cast<__nv_bfloat16*>(v);
     p.status = static_cast<int*>(workspace);
-    const int grid = row_blocks(p.c, sms);
+    const int grid = row_blocks(p.c);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (k_scales) launch_read<true>(p, grid, s);
     else launch_read<false>(p, grid, s);
