@@ -273,6 +273,8 @@ def _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu):
         raise ValueError("give k_scales and v_scales (8-bit pages) or neither (16-bit pages)")
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.shape[3] != HEAD_DIM:
         raise ValueError("k_pages must be [num_pages, kv_heads, page_size, 128]")
+    if not k_pages.is_cuda:
+        raise ValueError("k_pages must be a CUDA tensor")
     shape, dev = k_pages.shape, k_pages.device
     if k_scales is None:
         _check_as(k_pages, "k_pages", torch.float16, shape, dev)

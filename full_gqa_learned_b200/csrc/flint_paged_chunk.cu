@@ -447,7 +447,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             auto entry = [&](int ch) -> int {
                 if (SRC == kPcStaged) return lane == 0 ? 0 : -2;
                 const int pos = gr.kb + kKeyChunk * ch + lane * ps;
-                return lane < npg && pos < gr.hi ? __ldg(table + (pos >> c.ps_log2)) : -2;
+                return lane < npg && pos < gr.hi ? max(__ldg(table + (pos >> c.ps_log2)), -1) : -2;
             };
             int pg = entry(sg.t0);
             for (int ch = sg.t0; ch < sg.t1; ++ch) {
@@ -654,7 +654,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // ks + l: -1 none, -2 no position.
             auto page_of = [&](int ch) -> int {
                 const int pos = gr.kb + kKeyChunk * ch + 32 * w + lane;
-                return ch < sg.t1 && pos >= gr.lo && pos < gr.hi ? __ldg(table + (pos >> c.ps_log2)) : -2;
+                return ch < sg.t1 && pos >= gr.lo && pos < gr.hi ? max(__ldg(table + (pos >> c.ps_log2)), -1) : -2;
             };
             // Row of the pools, or -1.
             auto row_of = [&](int page, int ch) -> long long {

@@ -349,7 +349,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
             t.hi = hi;
             t.head = head;
             const int k = key + 16 * lane;
-            t.page = lane < TL::pieces && k < hi && k + 16 > lo ? __ldg(table + (k >> c.ps_log2)) : -2;
+            t.page = lane < TL::pieces && k < hi && k + 16 > lo ? max(__ldg(table + (k >> c.ps_log2)), -1) : -2;
             key += TL::tile;
             --left;
             return t;

@@ -447,6 +447,7 @@ FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pag
  *  max_new    at least the most new tokens of any sequence (else the device
  *             status becomes FLINT_ERR_INVALID_ARG); chooses the kernels.
  *  out        bf16 [T, 8 kv_heads x 128];  lse  fp32 [8 kv_heads, T] or NULL.
+ *             Neither may overlap an input.
  *  workspace  flint_attn_paged_workspace_bytes(...) bytes; not shared by
  *             calls that may overlap on the GPU.  For 8-bit pages and max_new
  *             > 8 that counts room (up to 512 MiB, else none) to expand the
