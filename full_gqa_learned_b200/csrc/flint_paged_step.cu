@@ -63,7 +63,16 @@ namespace flint {
 flint_status_t launch_paged_chunk(const PagedAttnParams& p, cudaStream_t s);
 
 constexpr int kStepWarps = 4;                            // consumer warps
-constexpr int kStepThreads = 32 * kStepWarps + 32;       // and the producer
+// Threads: the consumers and the producer.  Two tokens a group (NT = 2) take
+// more registers than two CTAs an SM leave each of 160 threads (168: they
+// spill), so there the producer is a warpgroup of one busy warp that gives its
+// registers to the consumers' (drafts of 2 to 6 tokens 55 us, 60 without; one
+// token a group has no use for it: 36 us become 38).
+template <int NT> struct StepShape {
+    static constexpr int threads = 32 * kStepWarps + (NT == 1 ? 32 : 128);
+    static constexpr uint32_t producer = 56, consumer = 200;
+};
+static_assert(128 * 56 + 128 * 200 <= 256 * 128, "register split");
 constexpr uint32_t kStepStages = 3;
 constexpr uint32_t kStepHalf = 16384;                    // a tile's keys, or values
 constexpr uint32_t kStepStage = 2 * kStepHalf;
@@ -204,7 +213,8 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     const PagedCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // a run of sequences a thread
-    const int per = (c.B + kStepThreads - 1) / kStepThreads, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
+    constexpr int kThreads = StepShape<NT>::threads;
+    const int per = (c.B + kThreads - 1) / kThreads, b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
     bool ill = false;
     long long sum = 0;
     if (b0 < b1) {
@@ -228,7 +238,7 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     *bad = __syncthreads_or(ill);
     long long before = inc - sum, total = 0;
 #pragma unroll
-    for (int x = 0; x < kStepThreads / 32; ++x) {
+    for (int x = 0; x < kThreads / 32; ++x) {
         if (x < warp) before += sm->scan[x];
         total += sm->scan[x];
     }
@@ -272,7 +282,7 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
 struct StepMaps { CUtensorMap k, v, k16, v16; };
 
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kStepThreads, kStepCtasPerSm)
+__global__ void __launch_bounds__(StepShape<NT>::threads, kStepCtasPerSm)
 paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p) {
     using S = StepSmem<NT>;
     using TL = StepTile<FP8>;
@@ -322,8 +332,15 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         *hi = g.p0 + g.nrows;
     };
 
-    if (warp == kStepWarps) {
-        // ============================================================ producer (the whole warp)
+    if (warp >= kStepWarps) {
+        // ============================================================ producer (a whole warp)
+        if constexpr (NT > 1) {
+            regs_dec<StepShape<NT>::producer>();
+            if (warp > kStepWarps) {
+                __syncthreads();
+                return;
+            }
+        }
         // Lane l < pieces holds piece l (16 positions) of a tile: its page, and
         // for 8-bit pages its scales, both fetched ahead.
         struct Tile { int key, lo, hi, head, page; bool any; };
@@ -420,6 +437,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
 
     // ================================================================ consumers
     // (their constants are fetched while the first tiles are on their way)
+    if constexpr (NT > 1) regs_inc<StepShape<NT>::consumer>();
     const int eq = prescale_exponent(warp_max_abs128(p.q_norm_w));
     const float C = ldexpf(1.4426950408889634f * 0.08838834764831845f, -eq);   // log2(e) / sqrt(128)
     const float qscale = ldexpf(1.f, eq);
@@ -926,7 +944,7 @@ cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStre
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
-    paged_step_kernel<NT, FP8><<<p.step_ctas, kStepThreads, StepSmem<NT>::total, s>>>(maps, p);
+    paged_step_kernel<NT, FP8><<<p.step_ctas, StepShape<NT>::threads, StepSmem<NT>::total, s>>>(maps, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
