@@ -12,7 +12,7 @@
 //   CTA may hold in part leave (m, l, O) in FP32, folded in CTA order by the
 //   combine kernel.  Few long sequences fill the GPU as well as many short
 //   ones, and the last CTA ends with the first.
-// * Warp 0 loads the raw query tiles and, for 16-bit pages, K and V by TMA:
+// * Warp 0 loads the raw query tiles and, for 16-bit pages, K by TMA, warp 3 V:
 //   a page's slots of one head are consecutive rows, so a box is a page (64
 //   channels x ps slots) and 128 / ps boxes fill a chunk's half tile.  Pages
 //   past the last position are not loaded.  Warp 2 writes zeros over the V
@@ -420,13 +420,31 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (tid == 0) reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = PagedNote{};
     } else if (warp < 4) {
       regs_dec<PcShape<FP8>::control>();
-      if (warp == 0) {
-        // ============================================================ producer (the whole warp)
+      if (warp == 0 || warp == 3) {
+        // ============================================================ producers: queries and K (warp 0), V (warp 3)
+        // (one warp for both would hold K back behind a V stage in use)
+        const bool is_k = warp == 0;
+        const uint32_t full = is_k ? PC_K_FULL : PC_V_FULL, empty = is_k ? PC_K_EMPTY : PC_V_EMPTY;
+        const uint32_t tile = sbase + (is_k ? kPcK : kPcV);
         uint32_t qph[2] = {0u, 0u}, st = 0, ph = 0, narm_q[2] = {0u, 0u}, narm = 0;
         bool ok = true;
         for (; ok && paged_share_next(share, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
-            const int ntile = sg.g.nrows > kTokPerTile ? 2 : 1;
+            if (!is_k && first && lane == 0) {
+                // a pair that the share begins inside of is held in part by the
+                // CTAs before, too: the first CTA of those leaves the combine a note
+                const long long W = hdr->chunk.tiles * ng, G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
+                PagedNote n = {};
+                if (sg.t0 > 0) {
+                    n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.g.tiles);
+                    n.fold = n.parts.cf == (int)blockIdx.x - 1;
+                    n.row = sg.g.row;
+                    n.head = sg.head;
+                    n.rows = kGroup * sg.g.nrows;
+                }
+                reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = n;
+            }
+            const int ntile = !is_k ? 0 : sg.g.nrows > kTokPerTile ? 2 : 1;
             for (int t = 0; t < ntile && ok; ++t) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_Q_EMPTY + t), qph[t] ^ 1, abort_flag, status));
                 if (!ok) break;
@@ -451,50 +469,33 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             int pg = entry(sg.t0);
             for (int ch = sg.t0; ch < sg.t1; ++ch) {
-                bool live = pg >= 0 && pg < c.num_pages;
+                const bool live = pg >= 0 && pg < c.num_pages;
                 if (!live && pg != -2) atomicCAS(status, 0, kStatusInvalid);
                 const int page = pg;
                 pg = ch + 1 < sg.t1 ? entry(ch + 1) : -2;
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * ps * kHD * 2;
                 const int y = SRC == kPcStaged ? sg.g.krow + kKeyChunk * ch : 0;
                 const int z = SRC == kPcStaged ? sg.head : live ? page * ng + sg.head : 0;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_K_EMPTY + st), ph ^ 1, abort_flag, status));
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(empty + st), ph ^ 1, abort_flag, status));
                 if (!ok) break;
-                if (lane == 0) mbar_expect_tx(bar(PC_K_FULL + st), bytes);
+                if (lane == 0) mbar_expect_tx(bar(full + st), bytes);
                 __syncwarp();
-                uint32_t dst = sbase + kPcK + st * kPcTile + lane * ps * 128;
+                const uint32_t dst = tile + st * kPcTile + lane * ps * 128;
                 if (live) {
-                    tma_load_3d(dst, &tm_k, bar(PC_K_FULL + st), 0, y, z);
-                    tma_load_3d(dst + kPcHalf, &tm_k, bar(PC_K_FULL + st), 64, y, z);
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_EMPTY + st), ph ^ 1, abort_flag, status));
-                if (!ok) {
-                    // this stage's K alone is armed; it lands without a V
-                    ++narm;
-                    break;
-                }
-                if (lane == 0) mbar_expect_tx(bar(PC_V_FULL + st), bytes);
-                __syncwarp();
-                dst = sbase + kPcV + st * kPcTile + lane * ps * 128;
-                if (live) {
-                    tma_load_3d(dst, &tm_v, bar(PC_V_FULL + st), 0, y, z);
-                    tma_load_3d(dst + kPcHalf, &tm_v, bar(PC_V_FULL + st), 64, y, z);
+                    tma_load_3d(dst, is_k ? &tm_k : &tm_v, bar(full + st), 0, y, z);
+                    tma_load_3d(dst + kPcHalf, is_k ? &tm_k : &tm_v, bar(full + st), 64, y, z);
                 }
                 ++narm;
                 st ^= 1; if (st == 0) ph ^= 1;
             }
         }
         // drain: every armed load has landed before shared memory is released
-        // (after a failed wait a stage's V may not have been armed: bounded)
         volatile int never = 0;
         const unsigned long long lim = 100ull * 1000ull * 1000ull;
         for (uint32_t t = 0; t < 2; ++t) {
             if (narm_q[t]) mbar_wait(bar(PC_Q_FULL + t), (narm_q[t] - 1) & 1, &never, nullptr, lim);
             const uint32_t n = (narm + 1 - t) / 2;     // stage t received loads number t, t + 2, ...
-            if (!FP8 && n) {
-                mbar_wait(bar(PC_K_FULL + t), (n - 1) & 1, &never, nullptr, lim);
-                mbar_wait(bar(PC_V_FULL + t), (n - 1) & 1, &never, nullptr, lim);
-            }
+            if (n) mbar_wait(bar(full + t), (n - 1) & 1, &never, nullptr, lim);
         }
       } else if (warp == 1) {
         // ============================================================ MMA issuer
@@ -590,22 +591,6 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_wait(bar(PC_DRAIN), 0, &never, nullptr, 100ull * 1000ull * 1000ull);
         }
         __syncwarp();
-      } else if (warp == 3) {
-        // ============================================================ the note for the combine kernel
-        if (paged_share_next(share, sg, true) && lane == 0) {
-            // a pair that the share begins inside of is held in part by the
-            // CTAs before, too: the first CTA of those leaves the combine a note
-            const long long W = hdr->chunk.tiles * ng, G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
-            PagedNote n = {};
-            if (sg.t0 > 0) {
-                n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.g.tiles);
-                n.fold = n.parts.cf == (int)blockIdx.x - 1;
-                n.row = sg.g.row;
-                n.head = sg.head;
-                n.rows = kGroup * sg.g.nrows;
-            }
-            reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = n;
-        }
       } else if (warp == 2 && !FP8) {
         // ============================================================ V rows without a position
         uint32_t st = 0, ph = 0;
