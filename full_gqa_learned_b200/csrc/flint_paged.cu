@@ -66,19 +66,23 @@ __device__ void paged_check_block(const PagedCache& c, int* status, bool keep_no
 
 // Places of the warp's tokens t0 .. t0 + n - 1 (n <= 32): lane i holds token
 // t0 + i's position and page, page -1 where it has none or belongs to nobody
-// (`own`: it belongs to a sequence's run).  One search a warp; lanes walk on
-// from there.
+// (`own`: it belongs to a sequence's run).  One search a warp, and one a lane
+// past its sequence's end.
 struct PagedPlace { int pos, page; bool own; };
 __device__ __forceinline__ PagedPlace paged_locate(const PagedCache& c, int t0, int n) {
     const int t = t0 + (threadIdx.x & 31);
     PagedPlace r = {0, -1, false};
     int b = warp_last_leq(c.cu, c.B, t0);
     if ((int)(threadIdx.x & 31) >= n || t >= c.T) return r;
-    int a = __ldg(c.cu + b), z = __ldg(c.cu + b + 1);
-    while (t >= z && b + 1 < c.B) {
-        a = z;
-        z = __ldg(c.cu + ++b + 1);
+    if (t >= __ldg(c.cu + b + 1)) {
+        // the last sequence that starts at t or before
+        int hi = c.B - 1;
+        while (b < hi) {
+            const int mid = (b + hi + 1) >> 1;
+            if (__ldg(c.cu + mid) <= t) b = mid; else hi = mid - 1;
+        }
     }
+    const int a = __ldg(c.cu + b), z = __ldg(c.cu + b + 1);
     const int L = __ldg(c.len + b);
     r.own = t < __ldg(c.cu + c.B);
     if (t < a || t >= z || L < 0) return r;
@@ -98,11 +102,11 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedCache& c, int t0, 
 __host__ __device__ inline int paged_tokens_per_warp(int T) { return T >= 16384 ? 8 : T >= 4096 ? 4 : T >= 2048 ? 2 : 1; }
 
 // E8M0 exponent e of a row whose largest magnitude is a.
-__device__ __forceinline__ int paged_exponent(float a) {
+__device__ __forceinline__ int paged_exponent(float a, int most) {
     const uint32_t u = __float_as_uint(a);
     const int E = (int)(u >> 23) - 127;                       // a = 1.m x 2^E
     const int e = E - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);   // 448 = 1.75 x 2^8
-    return min(max(e, kPagedEMin), kPagedEMax);
+    return min(max(e, kPagedEMin), most);
 }
 
 // Eight values x 2^-e as E4M3 codes (round to nearest even, saturating).
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
                 ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
                 av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
             }
-            const int ek = paged_exponent(ak), ev = paged_exponent(av);
+            const int ek = paged_exponent(ak, kPagedKeyEMax), ev = paged_exponent(av, kPagedEMax);
             const float ik = __uint_as_float((uint32_t)(127 - ek) << 23), iv = __uint_as_float((uint32_t)(127 - ev) << 23);
             if (ok) {
                 uint8_t* kd = static_cast<uint8_t*>(p.k_pages) + row * kHD + 8 * sub;
@@ -370,13 +374,13 @@ flint_status_t check_cache(PagedCache* c, const void* k_pages, const void* v_pag
         return fail(FLINT_ERR_INVALID_ARG, "kv_heads=%d: 1, 2 or 4", kv_heads);
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
         return fail(FLINT_ERR_UNSUPPORTED, "page_size=%d: 16, 32, 64 or 128 slots", page_size);
+    if ((k_scales == nullptr) != (v_scales == nullptr))
+        return fail(FLINT_ERR_INVALID_ARG, "give k_scales and v_scales (8-bit pages) or neither (16-bit pages)");
+    if (B == 0 || T == 0) return FLINT_OK;
     if (max_pages < 1 || max_pages > FLINT_MAX_TOKENS)
         return fail(FLINT_ERR_INVALID_ARG, "max_pages=%d outside [1, %d]", max_pages, FLINT_MAX_TOKENS);
     if (num_pages < 1 || (long long)num_pages * kv_heads > 0x7fffffffLL)
         return fail(FLINT_ERR_INVALID_ARG, "num_pages=%d", num_pages);
-    if ((k_scales == nullptr) != (v_scales == nullptr))
-        return fail(FLINT_ERR_INVALID_ARG, "give k_scales and v_scales (8-bit pages) or neither (16-bit pages)");
-    if (B == 0 || T == 0) return FLINT_OK;
     if (!k_pages || !v_pages || !table || !len || !cu) return fail(FLINT_ERR_INVALID_ARG, "null tensor pointer");
     if (!al(k_pages, 16) || !al(v_pages, 16) || !al(k_scales, 16) || !al(v_scales, 16))
         return fail(FLINT_ERR_INVALID_ARG, "the pages and their scales must be 16-byte aligned");

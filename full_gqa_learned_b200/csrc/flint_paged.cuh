@@ -23,6 +23,9 @@ namespace flint {
 // saturate).
 constexpr int kPagedEMin = -24;
 constexpr int kPagedEMax = 40;
+// Keys are read back and multiplied in FP16: 448 x 2^7 is the largest multiple
+// that no rounding takes out of its range.
+constexpr int kPagedKeyEMax = 7;
 
 struct PagedCache {
     const int* table;            // [B, max_pages]
@@ -172,6 +175,8 @@ struct PagedNote {
 struct PagedWs {
     size_t header, notes, spart, inv, groups, prefix, cpart, stage_k, stage_v, total;
 };
+// Row groups of a chunk call at most.
+__host__ __device__ inline size_t paged_groups(int B, int T) { return (size_t)T / kChunkTok + (B < T ? B : T); }
 __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas, int chunk_ctas, int stage_rows) {
     PagedWs L;
     size_t o = 256;
@@ -181,7 +186,7 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas,
         o = ws_align(o + sizeof(PagedNote) * (size_t)step_ctas, 256);
         L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
     } else {
-        const size_t n = (size_t)T / kChunkTok + (B < T ? B : T);
+        const size_t n = paged_groups(B, T);
         o = ws_align(o + sizeof(PagedNote) * (size_t)chunk_ctas, 256);
         L.inv = o;    o += 64 * sizeof(double);
         L.groups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);

@@ -204,6 +204,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
         if (b1 < c.B) off[b1 / every] = n_groups + ex;
         n_groups += tot;
     }
+    // ill-formed boundaries can name the same rows again and again; the groups
+    // have room for each row once
+    const int most = (int)paged_groups(c.B, c.T);
+    if (n_groups > most || n_groups < 0) {
+        n_groups = most;
+        s_bad = 1;
+    }
     __syncthreads();
     const int n_off = (c.B + every - 1) / every;
     long long tiles = 0;

@@ -168,9 +168,12 @@ __device__ __forceinline__ int step_tiles(const PagedAttnParams& p, int p0, int 
     const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
     return (p0 + nrows - step_base(p, lo, tile) + tile - 1) / tile;
 }
+// Enters sequence b (rows [a, z), cached positions len), or the next one with
+// new tokens; the whole warp calls it.  Runs of empty sequences are skipped by
+// one search: their boundaries are all z.
 __device__ __forceinline__ void step_enter(const PagedAttnParams& p, StepWalk& w, int b, int a, int z, int len) {
     const PagedCache& c = p.c;
-    for (;; ++b) {
+    for (;;) {
         const int n = paged_new(c, p.max_new, a, z, len);
         w.b = b;
         w.a = a;
@@ -181,8 +184,16 @@ __device__ __forceinline__ void step_enter(const PagedAttnParams& p, StepWalk& w
         w.len1 = more ? __ldg(c.len + b + 1) : 0;
         if (n > 0 || !more) return;
         a = z;
-        z = w.z1;
-        len = w.len1;
+        ++b;
+        if (w.z1 > a) {
+            z = w.z1;
+            len = w.len1;
+        } else {
+            b += warp_last_leq(c.cu + b, c.B - b, a);
+            a = __ldg(c.cu + b);
+            z = __ldg(c.cu + b + 1);
+            len = __ldg(c.len + b);
+        }
     }
 }
 template <int NT>

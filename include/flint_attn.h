@@ -376,7 +376,8 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  *             kv_heads, page_size] E8M0 bytes (scale 2^(byte - 127)), one a
  *             token and head: the value is code x scale.  The scale of a row
  *             with largest magnitude a is 2^e for the smallest e in [-24, 40]
- *             with a <= 448 x 2^e; larger values saturate.
+ *             with a <= 448 x 2^e (keys: [-24, 7], so that they fit FP16);
+ *             larger values saturate.
  *  page_table int32 [B, max_pages].
  *  cache_len  int32 [B]: positions cached before this call's new tokens.
  *  cu_new     int32 [B+1]: new token t, cu_new[b] <= t < cu_new[b+1], belongs
@@ -407,7 +408,7 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  *  workspace  FLINT_PAGED_STATUS_BYTES bytes.
  * A page table entry of -1 drops the token (a sliding layer keeps no page
  * for positions that no later token sees).  A slot that several tokens of one
- * call name (a page listed twice) ends up with the rows of any of them.
+ * call name (a page listed twice) ends up undefined.
  * Infinite elements saturate in 8-bit pages; NaN stays NaN.
  */
 FLINT_API flint_status_t flint_paged_append(const void* k, const void* v, const float* k_norm_w,
@@ -455,8 +456,8 @@ FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pag
  *             size for 16-bit pages (eight_bit == 0) is accepted, too: the
  *             call then converts on chip, with the same result, in about twice
  *             the time.
- * Cached values and keys at positions a token sees must be finite and scales
- * within 2^-24 .. 2^40; slots of other positions may hold anything, and page
+ * Cached values and keys at positions a token sees must be finite, keys within
+ * FP16's range, and scales within 2^-24 .. 2^40; slots of other positions may hold anything, and page
  * table entries that no new token's window touches are not read.
  * Results do not depend on timing: every sum has a fixed order.
  */

@@ -7,8 +7,8 @@ never imports it.
 Position p of sequence b lives in page table[b, p // ps], slot p % ps of
 pools [P, g, ps, 128].  16-bit pages hold k~ = RoPE(RMSNorm(k, w_k), p)
 rounded to FP16 and v in BF16; 8-bit pages hold E4M3 codes with a scale 2^e
-per token and head, e the smallest integer in [-24, 40] with max|x| <=
-448 x 2^e.  New row i of sequence b (position p = len[b] + i) attends to the
+per token and head, e the smallest integer in [-24, 40] (keys: [-24, 7]) with
+max|x| <= 448 x 2^e.  New row i of sequence b (position p = len[b] + i) attends to the
 positions max(0, p - W + 1) .. p (W = 0: from 0) as the pages hold them, and
 to the learned sink (FlintAttention.forward and _apply_rope on the NeMo
 AutoModel "flint.layers" API page; HF discussion #26 on RecursiveSI/flint):
@@ -51,9 +51,9 @@ def e4m3(x):
     return np.clip(np.round(x / step) * step, -448.0, 448.0)
 
 
-def quantise(x):
-    """(code values, exponents) of rows x [..., 128]."""
-    e = scale_exponent(x)
+def quantise(x, most=E_MAX):
+    """(code values, exponents) of rows x [..., 128]; keys: most = 7."""
+    e = np.minimum(scale_exponent(x), most)
     return e4m3(x * np.exp2(-e.astype(np.float64))[..., None]), e
 
 

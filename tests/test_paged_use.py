@@ -213,7 +213,7 @@ def test_bad_pages_are_reported_and_not_read(fa, page, new, fp8):  # noqa: F811
     assert (k[32:48] == 0).all() and (v[32:48] == 0).all() and (k[48:100] != 0).any()
 
 
-@pytest.mark.parametrize("what", ["cu_start", "cu_down", "cu_past", "len_neg", "len_past", "table_past", "max_new"])
+@pytest.mark.parametrize("what", ["cu_start", "cu_down", "cu_repeats", "cu_past", "len_neg", "len_past", "table_past", "max_new"])
 @pytest.mark.parametrize("new", [[1, 1, 1], [2, 40, 1]])
 def test_ill_formed_calls_are_reported(fa, what, new):  # noqa: F811
     c = Case([100, 50, 20], new, ps=16, seed=21)
@@ -225,6 +225,15 @@ def test_ill_formed_calls_are_reported(fa, what, new):  # noqa: F811
         t["cu"][0] = 1
     elif what == "cu_down":
         t["cu"][1] = -3
+    elif what == "cu_repeats":                            # the same rows named over and over
+        B = 300
+        t["cu"] = torch.tensor([0, c.T] * (B // 2) + [0], dtype=torch.int32, device="cuda")
+        t["ctx"] = torch.full((B,), 5, dtype=torch.int32, device="cuda")
+        t["table"] = t["table"][:1].repeat(B, 1).clamp(min=0)
+        mn = c.T
+        st, _, _ = attend(fa, c, t, max_new=mn)
+        assert st == INVALID and append(fa, c, t) == INVALID
+        return
     elif what == "cu_past":
         t["cu"][3] = c.T + 1000
     elif what == "len_neg":
@@ -258,19 +267,30 @@ def test_nobody_has_new_tokens(fa):  # noqa: F811
 
 
 @pytest.mark.parametrize("mn", [2, 64])
-def test_many_sequences(fa, mn):  # noqa: F811
+@pytest.mark.parametrize("B,share", [(5000, 0.05), (40000, 0.002)])
+def test_many_sequences(fa, mn, B, share):  # noqa: F811
     """More sequences than a plan's threads, most without new tokens."""
     r = np.random.default_rng(23)
-    B = 5000
-    ctx = r.integers(0, 20, B)
-    new = np.where(r.random(B) < 0.05, r.integers(1, 3, B), 0)
-    new[17], new[4999] = 2, 1
+    ctx = np.where(r.random(B) < 0.1, r.integers(0, 20, B), 0)
+    new = np.where(r.random(B) < share, r.integers(1, 3, B), 0)
+    new[17], new[B - 1] = 2, 1
     c = Case([int(x) for x in ctx], [int(x) for x in new], g=1, ps=16, seed=24)
     t = c.to("cuda")
     assert append(fa, c, t) == 0
     st, out, lse = attend(fa, c, t, max_new=mn)
     assert st == 0
     check_attend(c, t, out, lse, chunk=mn > 8)
+
+
+def test_keys_saturate_within_fp16(fa):  # noqa: F811
+    """Norm weights far beyond any model's: keys stay finite in both formats."""
+    for fp8, top in ((False, 65504.0), (True, 57344.0)):
+        c = Case([3], [2], fp8=fp8, seed=27, w_scale=4e4)
+        t = c.to("cuda")
+        assert append(fa, c, t) == 0
+        cu = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+        k, _ = fa.paged_read(t["k_pages"], t["v_pages"], t["table"], t["ctx"], cu, 2, **scales(t))
+        assert torch.isfinite(k).all() and k.abs().max().item() == top
 
 
 def test_offsets_past_32_bits(fa):  # noqa: F811
