@@ -293,22 +293,42 @@ def _check_pages(k_pages, v_pages, k_scales, v_scales, page_table, start, cu):
     return dev, B, shape[1], shape[2]
 
 
-def _paged_call(fn, args, workspace, dev, stream, own):
-    """Runs fn(*args, workspace, its bytes, stream) on dev.  Tensors that the
-    call allocated on torch's current stream (own) are kept until another
-    stream has passed them."""
+def _paged_stream(stream, dev):
+    """(its cudaStream_t, None) where stream is torch's current one on dev or
+    not given, (its cudaStream_t, the stream) for another."""
     import torch
-    if workspace.__class__ is not torch.Tensor or workspace.dtype is not torch.uint8:
-        _check(workspace, "workspace", torch.uint8)
-    current = torch.cuda.current_stream(dev)
-    ptr = current.cuda_stream
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
-        if stream.cuda_stream != ptr:
-            ptr = stream.cuda_stream
-            for t in own:
-                t.record_stream(stream)
+    # the number alone: torch.cuda.current_stream builds an object first (2 us of a call's 20)
+    current = torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream is None:
+        return current, None
+    ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if ptr == current:
+        return current, None
+    return ptr, torch.cuda.ExternalStream(ptr, device=dev)
+
+
+def _paged_new(like, shape, dtype, side):
+    """An unset tensor that the call may use on its stream at once: with
+    another stream than torch's current one (side) it is that stream's memory
+    (the current stream's may still be in use by what was queued there
+    before), kept until the current stream has passed it too."""
+    if side is None:
+        return like.new_empty(shape, dtype=dtype)
+    import torch
+    current = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(side):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(current)
+    return t
+
+
+def _paged_call(fn, args, empty, workspace, dev, ptr, side):
+    """Runs fn(*args, workspace, its bytes, stream) on dev.  A call without
+    sequences or tokens (empty) launches nothing; its status is FLINT_OK."""
+    import torch
+    if empty:
+        with torch.cuda.stream(side):                     # None: torch's current stream
+            workspace[:PAGED_STATUS_BYTES].zero_()
     args += (workspace.data_ptr(), workspace.numel(), ptr)
     if torch.cuda.current_device() == dev.index:
         st = fn(*args)
@@ -341,15 +361,16 @@ def paged_append(k, v, k_norm_w, k_pages, v_pages, page_table, cache_len, cu_new
     _check_as(k, "k", torch.bfloat16, (T, g, HEAD_DIM), dev)
     _check_as(v, "v", torch.bfloat16, (T, g, HEAD_DIM), dev)
     _check_as(k_norm_w, "k_norm_w", torch.float32, (HEAD_DIM,), dev)
-    own = []
+    ptr, side = _paged_stream(stream, dev)
     if workspace is None:
-        workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
-        own.append(workspace)
-    _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        workspace = _paged_new(k, PAGED_STATUS_BYTES, torch.uint8, side)
+    else:
+        _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _paged_call(lib.flint_paged_append, (
         k.data_ptr(), v.data_ptr(), k_norm_w.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
         _ptr(v_scales), page_table.data_ptr(), cache_len.data_ptr(), cu_new.data_ptr(), B, T, page_table.shape[1],
-        k_pages.shape[0], ps, g, int(bool(use_rope)), float(rope_theta), float(eps)), workspace, dev, stream, own)
+        k_pages.shape[0], ps, g, int(bool(use_rope)), float(rope_theta), float(eps)),
+        not (B and T), workspace, dev, ptr, side)
     paged_append.last_workspace = workspace
 
 
@@ -367,23 +388,23 @@ def paged_read(k_pages, v_pages, page_table, start, cu_out, T: int, *, k_scales=
     T = int(T)
     if T < 0:
         raise ValueError("T must not be negative")
-    own = []
+    ptr, side = _paged_stream(stream, dev)
     if k is None:
-        k = torch.empty((T, g, HEAD_DIM), dtype=torch.float16, device=dev)
-        own.append(k)
+        k = _paged_new(k_pages, (T, g, HEAD_DIM), torch.float16, side)
+    else:
+        _check_as(k, "k", torch.float16, (T, g, HEAD_DIM), dev)
     if v is None:
-        v = torch.empty((T, g, HEAD_DIM), dtype=torch.bfloat16, device=dev)
-        own.append(v)
+        v = _paged_new(k_pages, (T, g, HEAD_DIM), torch.bfloat16, side)
+    else:
+        _check_as(v, "v", torch.bfloat16, (T, g, HEAD_DIM), dev)
     if workspace is None:
-        workspace = torch.empty(PAGED_STATUS_BYTES, dtype=torch.uint8, device=dev)
-        own.append(workspace)
-    _check_as(k, "k", torch.float16, (T, g, HEAD_DIM), dev)
-    _check_as(v, "v", torch.bfloat16, (T, g, HEAD_DIM), dev)
-    _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        workspace = _paged_new(k_pages, PAGED_STATUS_BYTES, torch.uint8, side)
+    else:
+        _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _paged_call(lib.flint_paged_read, (
         k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales), page_table.data_ptr(),
         start.data_ptr(), cu_out.data_ptr(), B, T, page_table.shape[1], k_pages.shape[0], ps, g, k.data_ptr(),
-        v.data_ptr()), workspace, dev, stream, own)
+        v.data_ptr()), not (B and T), workspace, dev, ptr, side)
     paged_read.last_workspace = workspace
     return k, v
 
@@ -412,28 +433,25 @@ def attn_paged(q, q_norm_w, sinks, k_pages, v_pages, page_table, cache_len, cu_n
     _check_as(q_norm_w, "q_norm_w", torch.float32, (HEAD_DIM,), dev)
     _check_as(sinks, "sinks", torch.float32, (nh,), dev)
     max_new, window, width = int(max_new), int(window), page_table.shape[1]
-    own = []
+    ptr, side = _paged_stream(stream, dev)
     if out is None:
-        out = torch.empty((T, nh * HEAD_DIM), dtype=torch.bfloat16, device=dev)
-        own.append(out)
+        out = _paged_new(q, (T, nh * HEAD_DIM), torch.bfloat16, side)
     else:
         _check_as(out, "out", torch.bfloat16, (T, nh * HEAD_DIM), dev)
     if lse is None and want_lse:
-        lse = torch.empty((nh, T), dtype=torch.float32, device=dev)
-        own.append(lse)
+        lse = _paged_new(q, (nh, T), torch.float32, side)
     elif lse is not None:
         _check_as(lse, "lse", torch.float32, (nh, T), dev)
     if workspace is None:
         need = lib.flint_attn_paged_workspace_bytes(B, T, max_new, width, ps, g, window, k_scales is not None)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        own.append(workspace)
+        workspace = _paged_new(q, max(need, PAGED_STATUS_BYTES), torch.uint8, side)
     else:
         _check_as(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _paged_call(lib.flint_attn_paged, (
         q.data_ptr(), q_norm_w.data_ptr(), sinks.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
         _ptr(v_scales), page_table.data_ptr(), cache_len.data_ptr(), cu_new.data_ptr(), B, T, max_new, width,
         k_pages.shape[0], ps, g, window, int(bool(use_rope)), float(rope_theta), float(eps), out.data_ptr(),
-        _ptr(lse)), workspace, dev, stream, own)
+        _ptr(lse)), not (B and T), workspace, dev, ptr, side)
     attn_paged.last_workspace = workspace
     return out, lse
 

@@ -151,6 +151,54 @@ def test_calls_on_two_streams(fa):  # noqa: F811
         check_attend(c, t, o, l, chunk=c.new.max() > 8)
 
 
+def test_another_stream_gets_its_own_memory(fa):  # noqa: F811
+    """What the call allocates must not be memory that the current stream has
+    freed on the host and still writes on the device."""
+    c = Case([300, 20], [1, 2], seed=28)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    _, want, wl = attend(fa, c, t)
+    cu = torch.tensor([0, 300, 320], dtype=torch.int32, device="cuda")
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    wk, wv = fa.paged_read(t["k_pages"], t["v_pages"], t["table"], at, cu, 320)
+    side = torch.cuda.Stream()
+    busy = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(40):
+        busy.fill_(1)                                     # about 6 ms of the current stream
+    for like in (want, wl, wk, wv):
+        for _ in range(3):
+            torch.empty_like(like).fill_(7)
+    got = fa.attn_paged(t["q"], t["wq"], t["sinks"], t["k_pages"], t["v_pages"], t["table"], t["ctx"], t["cu"], max_new=2,
+                        window=0, use_rope=False, stream=side)
+    read = fa.paged_read(t["k_pages"], t["v_pages"], t["table"], at, cu, 320, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], wl)
+    assert torch.equal(read[0], wk) and torch.equal(read[1], wv)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_empty_calls_have_a_status(fa, given):  # noqa: F811
+    """No sequences, or no tokens: nothing is launched, and the status is not
+    an earlier call's."""
+    c = Case([20, 5], [1, 2], seed=29)
+    t = c.to("cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for B, T in ((0, 0), (0, 3), (2, 0)):
+        table, at, cu = t["table"][:B], torch.zeros(B, **i32), torch.zeros(B + 1, **i32)
+        kw = {}
+        if given:
+            kw["workspace"] = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        else:
+            torch.full((256,), 255, dtype=torch.uint8, device="cuda")       # what the allocator hands out next
+        fa.paged_append(t["k"][:T], t["v"][:T], t["wk"], t["k_pages"], t["v_pages"], table, at, cu, **kw)
+        assert fa.device_status(fa.paged_append.last_workspace) == 0
+        k, v = fa.paged_read(t["k_pages"], t["v_pages"], table, at, cu, T, **kw)
+        assert fa.device_status(fa.paged_read.last_workspace) == 0 and k.shape == v.shape == (T, 4, 128)
+        out, lse = fa.attn_paged(t["q"][:T], t["wq"], t["sinks"], t["k_pages"], t["v_pages"], table, at, cu, max_new=1, **kw)
+        assert fa.device_status(fa.attn_paged.last_workspace) == 0 and out.shape == (T, 4096) and lse.shape == (32, T)
+
+
 def test_sequences_share_prefix_pages(fa):  # noqa: F811
     """Two sequences whose first pages are the same page."""
     c = Case([64, 64], [1, 1], ps=16, seed=16)
