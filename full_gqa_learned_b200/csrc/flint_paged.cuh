@@ -121,21 +121,23 @@ struct PagedGroup {
 };
 
 // The work of one kernel: the tiles of all (group, KV head) pairs in a row,
-// group by group, head by head.  CTA c of G takes tiles [W c / G, W (c + 1) /
-// G) of the W = tiles x heads, so every CTA has the same number for any mix of
-// lengths, and holds at most two pairs in part.  For the chunk kernel a plan
-// kernel writes the groups and the exclusive prefix of their tile counts
-// (prefix[n] = tiles); the step kernel's CTAs work it out themselves.
-struct PagedList { long long tiles; int n, pad; };
-
+// group by group, head by head.  Every CTA takes a run of them, so it holds at
+// most two pairs in part.  The step kernel's CTA c of G takes tiles [W c / G,
+// W (c + 1) / G) of the W = tiles x heads and works that out itself; for the
+// chunk kernel a plan kernel writes the groups and where every CTA starts.
 struct PagedPlanHeader {
     int status;                  // device-side status (0 = ok)
-    int pad0;
-    PagedList chunk;
-    int pad[58];
+    int pad[63];
 };
 static_assert(sizeof(PagedPlanHeader) == 256, "plan header");
 
+// Where a chunk CTA's share starts: tile x of all, tile off of pair (gi, head).
+struct PagedStart {
+    long long x;
+    int gi, head, off, pad;
+};
+
+constexpr int kPagedMaxSms = 148;        // SMs that a call's shares are cut for
 constexpr int kChunkTok = 32;            // new tokens of a chunk kernel's group
 constexpr int kPagedStepRows = 16;       // query rows of a step partial
 // floats of a step partial: m[16], l[16], O[16][128]; of a chunk partial:
@@ -173,7 +175,7 @@ struct PagedNote {
 // Workspace of an attention call: of the step kernel (chunk_ctas == 0) a note
 // and two partials a CTA, of the chunk kernel the plan and two partials a CTA.
 struct PagedWs {
-    size_t header, notes, spart, inv, groups, prefix, cpart, stage_k, stage_v, total;
+    size_t header, notes, spart, inv, starts, groups, prefix, cpart, stage_k, stage_v, total;
 };
 // Row groups of a chunk call at most.
 __host__ __device__ inline size_t paged_groups(int B, int T) { return (size_t)T / kChunkTok + (B < T ? B : T); }
@@ -181,7 +183,7 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas,
     PagedWs L;
     size_t o = 256;
     L.header = 0;
-    L.notes = L.spart = L.inv = L.groups = L.prefix = L.cpart = L.stage_k = L.stage_v = o;
+    L.notes = L.spart = L.inv = L.starts = L.groups = L.prefix = L.cpart = L.stage_k = L.stage_v = o;
     if (chunk_ctas == 0) {
         o = ws_align(o + sizeof(PagedNote) * (size_t)step_ctas, 256);
         L.spart = o; o = ws_align(o + sizeof(float) * 2 * (size_t)step_ctas * kStepPart, 256);
@@ -189,6 +191,7 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas,
         const size_t n = paged_groups(B, T);
         o = ws_align(o + sizeof(PagedNote) * (size_t)chunk_ctas, 256);
         L.inv = o;    o += 64 * sizeof(double);
+        L.starts = o; o = ws_align(o + sizeof(PagedStart) * ((size_t)chunk_ctas + 1), 256);
         L.groups = o; o = ws_align(o + sizeof(PagedGroup) * n, 256);
         L.prefix = o; o = ws_align(o + sizeof(long long) * (n + 1), 256);
         L.cpart = o;  o = ws_align(o + sizeof(float) * 2 * (size_t)chunk_ctas * kChunkPart, 256);
@@ -229,8 +232,7 @@ __device__ __forceinline__ void paged_finish(float M, float L, float sink, float
 // A CTA's share, walked pair by pair.  The pair's place among all W tiles is
 // needed only where it is held in part (paged_seg_begin).
 struct PagedShare {
-    const PagedGroup* groups;
-    int ng, gi, head, off;       // the next pair; off: tile of it that the share enters at
+    int gi, head, off;           // the next pair; off: tile of it that the share enters at
     int left;                    // tiles left in the share
 };
 struct PagedSeg {
@@ -239,25 +241,17 @@ struct PagedSeg {
     bool whole;                  // all of it
     bool first;                  // the share's first pair
 };
-__device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedList& l, const PagedGroup* groups,
-                                                  const long long* prefix, int ng, int cta, int ctas) {
-    const long long W = l.tiles * ng;
-    const long long G = W < (long long)ctas ? W : (long long)ctas;
-    if (cta >= G) return false;
-    const long long t = W * cta / G;
-    s.groups = groups;
-    s.ng = ng;
-    s.left = (int)(W * (cta + 1) / G - t);
-    s.gi = warp_last_leq(prefix, l.n, t / ng);
-    const long long in = t - prefix[s.gi] * ng;
-    const int tiles = groups[s.gi].tiles;
-    s.head = (int)(in / tiles);
-    s.off = (int)(in - (long long)s.head * tiles);
-    return true;
+__device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedStart* starts, int cta) {
+    const PagedStart at = starts[cta];
+    s.gi = at.gi;
+    s.head = at.head;
+    s.off = at.off;
+    s.left = (int)(starts[cta + 1].x - at.x);
+    return s.left > 0;
 }
-__device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g, bool first) {
+__device__ __forceinline__ bool paged_share_next(PagedShare& s, const PagedGroup* groups, int ng, PagedSeg& g, bool first) {
     if (s.left <= 0) return false;
-    g.g = s.groups[s.gi];
+    g.g = groups[s.gi];
     g.gi = s.gi;
     g.head = s.head;
     g.t0 = s.off;
@@ -266,7 +260,7 @@ __device__ __forceinline__ bool paged_share_next(PagedShare& s, PagedSeg& g, boo
     g.first = first;
     s.left -= g.t1 - g.t0;
     s.off = 0;
-    if (++s.head == s.ng) { s.head = 0; ++s.gi; }
+    if (++s.head == ng) { s.head = 0; ++s.gi; }
     return true;
 }
 }  // namespace flint

@@ -7,11 +7,11 @@
 // * A group is 32 new tokens of one sequence, a tile 16 tokens x 8 query heads
 //   = 128 rows; chunks of 128 positions start at the page that holds the
 //   first position any row sees, so a chunk is a whole number of pages.
-//   Persistent CTAs share the chunks of all (group, KV head) pairs equally
-//   (PagedShare): a pair inside one CTA is written at once, the two pairs a
-//   CTA may hold in part leave (m, l, O) in FP32, folded in CTA order by the
-//   combine kernel.  Few long sequences fill the GPU as well as many short
-//   ones, and the last CTA ends with the first.
+//   Persistent CTAs share the chunks of all (group, KV head) pairs so that
+//   each has the same work (PagedShare): a pair inside one CTA is written at
+//   once, the two pairs a CTA may hold in part leave (m, l, O) in FP32, folded
+//   in CTA order by the combine kernel.  Few long sequences fill the GPU as
+//   well as many short ones, and the last CTA ends with the first.
 // * Warp 0 loads the raw query tiles and, for 16-bit pages, K by TMA, warp 3 V:
 //   a page's slots of one head are consecutive rows, so a box is a page (64
 //   channels x ps slots) and 128 / ps boxes fill a chunk's half tile.  Pages
@@ -23,7 +23,9 @@
 //   into rows of their own, loaded like pages of any size.  Otherwise a third
 //   warpgroup does the same chunk by chunk, into the swizzled layout that the
 //   tensor core reads; it does so again for every group of 32 tokens, and four
-//   warps need 6 to 9 us a chunk where the products and the softmax take 4.
+//   warps need 5 to 7 us a chunk where the products and the softmax take 3 to 4
+//   (their 120 registers hold a chunk's codes on the way: with 104, 766 us for 128
+//   sequences of 1 to 16 tokens over up to 6,000 positions, with 120, 566).
 // * Warp 1 issues S = Q K^T and O += P V per chunk and tile; warps 4-7 and
 //   8-11 are the softmax warpgroups of the two tiles (one thread a row): RMS
 //   norm and rotation of the queries in place as FP16 when a tile lands, then
@@ -33,10 +35,10 @@
 //   stays within 2^8.  A group of at most 16 rows runs on one tile alone.
 // Every wait is bounded (FLINT_ERR_TIMEOUT in the status word, abort, drain).
 //
-// Measured: 2,048 tokens over 32,049 positions, 16-bit pages: 1,186 us, 878 TF/s,
+// Measured: 2,048 tokens over 32,049 positions, 16-bit pages: 1,179 us, 883 TF/s,
 // 0.53 of the measured bf16 rate, as the forward kernel (its softmax and tensor
 // pipe take turns); four chunks of 257 to 512 tokens over up to 8,703 positions of
-// 8-bit pages 259 us, of which the expansion, the plan and the combine are 20.
+// 8-bit pages 255 us, of which the expansion, the plan and the combine are 20.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cmath>
@@ -57,7 +59,8 @@ constexpr uint32_t kPcStageBytes = 32 * 128;
 constexpr uint32_t kPcBar = kPcStage + 8 * kPcStageBytes;
 constexpr uint32_t kPcMisc = kPcBar + 32 * 8;
 constexpr uint32_t kPcWq = kPcMisc + 64;             // q_norm weight (128 floats)
-constexpr uint32_t kPcSmem = kPcWq + kHD * 4 + 1024; // + alignment slack
+constexpr uint32_t kPcWalk = kPcWq + kHD * 4;         // the converting warps' places in the share
+constexpr uint32_t kPcSmem = kPcWalk + 4 * 16 + 1024; // + alignment slack
 static_assert(kPcSmem <= 232448, "shared memory per block");
 // RoPE table of a softmax warp's 4 tokens: per token 32 frequency pairs {cos,
 // cos, sin, sin} (16 bytes), then 32 pairs {-sin, -sin}; rows padded
@@ -84,10 +87,11 @@ struct PcMisc {
 enum PcSource { kPcPages, kPcCodes, kPcStaged };
 template <bool FP8> struct PcShape {
     static constexpr int threads = FP8 ? 512 : 384;
-    static constexpr uint32_t control = FP8 ? 40 : 80, softmax = FP8 ? 184 : 208, convert = 104;
+    static constexpr uint32_t control = FP8 ? 40 : 80, softmax = FP8 ? 176 : 208, convert = 120;
 };
 static_assert(128 * 80 + 256 * 208 <= 384 * 168, "register split");
-static_assert(128 * 40 + 128 * 104 + 256 * 184 <= 512 * 128, "register split, 8-bit pages");
+static_assert(128 * 40 + 128 * 120 + 256 * 176 <= 512 * 128, "register split, 8-bit pages");
+static_assert(PcShape<true>::convert <= 128, "setmaxnreg.dec cannot raise the launch's 128");
 
 __device__ __forceinline__ float pc_ex2(float x) {
     float y;
@@ -170,16 +174,22 @@ __device__ __forceinline__ int plan_new(const PagedAttnParams& p, int b, bool* b
     return max(n, 0);
 }
 
-// One block: checks the boundaries and lengths, writes the groups with the
-// exclusive prefix of their chunk counts, and leaves the rotation frequencies.
+// One block: checks the boundaries and lengths, writes the groups, where every
+// CTA's share of their chunks starts and the combine's notes, and leaves the
+// rotation frequencies.
 // Group offsets of the sequences are kept in shared memory; past kPlanSeqs
 // sequences only every `every`-th is, and the rest is walked.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 4096;
+// A chunk takes about 3 us, a pair's query prologue and epilogue 5 to 6.  24
+// sequences with 1 to 384 new tokens, window 513 (2,049), over up to 40,000
+// positions of 16-bit pages: shares by chunks alone 139 us (330), pairs as 1
+// chunk 130 (287), as 1.5 122 (281), as 2 125 (279), as 4 131 (270).
+constexpr long long kCostChunk = 2, kCostPair = 3;
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p) {
     griddep_launch_dependents();
     __shared__ int s_bad, sh_i[32], off[kPlanSeqs];
-    __shared__ long long sh_l[32];
+    __shared__ long long sh_l[32], sh_prefix[kPlanThreads], sh_start[kPagedMaxSms + 1];
     const int tid = threadIdx.x;
     const PagedCache& c = p.c;
     const PagedWs L = paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, p.stage_rows);
@@ -187,27 +197,29 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
     double* inv = reinterpret_cast<double*>(p.ws + L.inv);
     PagedGroup* groups = reinterpret_cast<PagedGroup*>(p.ws + L.groups);
     long long* prefix = reinterpret_cast<long long*>(p.ws + L.prefix);
+    PagedStart* starts = reinterpret_cast<PagedStart*>(p.ws + L.starts);
+    PagedNote* notes = reinterpret_cast<PagedNote*>(p.ws + L.notes);
     if (tid == 0) s_bad = (c.cu[0] != 0 || c.cu[c.B] > c.T) ? 1 : 0;
     if (p.use_rope && tid < 64) inv[tid] = exp2(-(double)tid / 64.0 * log2((double)p.rope_theta));
     __syncthreads();
     const int every = (c.B + kPlanSeqs - 1) / kPlanSeqs;
     const int page_mask = (1 << c.ps_log2) - 1;
+    // ill-formed boundaries can name the same rows again and again; the groups
+    // have room for each row once (counts stop one above it)
+    const int most = (int)paged_groups(c.B, c.T);
     int n_groups = 0;
     for (int b0 = 0; b0 < c.B; b0 += kPlanThreads * every) {
         const int b1 = b0 + tid * every;
         int cnt = 0;
         bool bad = false;
-        for (int b = b1; b < min(b1 + every, c.B); ++b) cnt += (plan_new(p, b, &bad) + kChunkTok - 1) / kChunkTok;
+        for (int b = b1; b < min(b1 + every, c.B); ++b) cnt = min(cnt + (plan_new(p, b, &bad) + kChunkTok - 1) / kChunkTok, most + 1);
         if (bad) s_bad = 1;
         int tot;
         const int ex = plan_scan(cnt, sh_i, &tot);
         if (b1 < c.B) off[b1 / every] = n_groups + ex;
-        n_groups += tot;
+        n_groups = min(n_groups + tot, most + 1);
     }
-    // ill-formed boundaries can name the same rows again and again; the groups
-    // have room for each row once
-    const int most = (int)paged_groups(c.B, c.T);
-    if (n_groups > most || n_groups < 0) {
+    if (n_groups > most) {
         n_groups = most;
         s_bad = 1;
     }
@@ -250,13 +262,79 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
             groups[g] = r;
             prefix[g] = tiles + ex;
         }
+        if (g0 == 0) sh_prefix[tid] = ex;
         tiles += tot;
     }
     if (tid == 0) {
         prefix[n_groups] = tiles;
-        hdr->chunk.n = n_groups;
-        hdr->chunk.tiles = tiles;
         hdr->status = s_bad ? kStatusInvalid : kStatusOk;
+    }
+    __syncthreads();
+    // Where the CTAs start.  A pair costs its chunks and its prologue and
+    // epilogue; where a share is too short for every CTA to get a chunk that
+    // way, chunks alone count.
+    const long long all = tiles * c.ng;
+    long long W = c.ng * (kCostChunk * tiles + kCostPair * n_groups), a = kCostChunk, o = kCostPair, G = p.chunk_ctas;
+    if (W / G < a + o) {
+        W = all;
+        a = 1;
+        o = 0;
+        G = min(W, G);
+    }
+    for (int x = tid; x <= p.chunk_ctas; x += kPlanThreads) {
+        PagedStart st = {all, n_groups, 0, 0, 0};
+        const long long pos = x < G ? W * x / G : W;
+        if (pos < W) {
+            auto pre = [&](int g) { return g == n_groups ? tiles : n_groups <= kPlanThreads ? sh_prefix[g] : prefix[g]; };
+            int lo = 0, hi = n_groups - 1;                    // last group that starts at or before pos
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (c.ng * (a * pre(mid) + o * mid) <= pos) lo = mid; else hi = mid - 1;
+            }
+            const long long g0 = pre(lo), k = pre(lo + 1) - g0, in = pos - c.ng * (a * g0 + o * lo), w = a * k + o;
+            const int head = (int)(in / w);
+            const long long off = max(in - head * w - o + a - 1, 0ll) / a;       // a chunk belongs to whose share holds its first unit
+            st.x = g0 * c.ng + head * k + off;
+            st.gi = lo;
+            st.head = head;
+            st.off = (int)off;
+            if (off == k) {                                   // the next pair's first
+                st.off = 0;
+                if (++st.head == c.ng) {
+                    st.head = 0;
+                    ++st.gi;
+                }
+            }
+        }
+        starts[x] = st;
+        sh_start[x] = st.x;
+    }
+    __syncthreads();
+    // A pair that a share begins inside of is held in part by the CTAs before,
+    // too: the first CTA of those leaves the combine a note.
+    for (int x = tid; x < p.chunk_ctas; x += kPlanThreads) {
+        const PagedStart st = starts[x];
+        PagedNote n = {};
+        if (sh_start[x + 1] > st.x && st.off > 0) {
+            const PagedGroup g = groups[st.gi];
+            auto owner = [&](long long tile) {                // the CTA that holds it
+                int lo = 0, hi = p.chunk_ctas - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (sh_start[mid] <= tile) lo = mid; else hi = mid - 1;
+                }
+                return lo;
+            };
+            const long long seg = st.x - st.off;
+            n.parts.cf = owner(seg);
+            n.parts.cl = owner(seg + g.tiles - 1);
+            n.parts.second = sh_start[n.parts.cf] < seg;
+            n.fold = n.parts.cf == x - 1;
+            n.row = g.row;
+            n.head = st.head;
+            n.rows = kGroup * g.nrows;
+        }
+        notes[x] = n;
     }
 }
 
@@ -424,12 +502,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     PagedShare share;
     PagedSeg sg;
     bool first = true;
-    const bool work = paged_share_begin(share, hdr->chunk, reinterpret_cast<const PagedGroup*>(p.ws + L.groups),
-                                        reinterpret_cast<const long long*>(p.ws + L.prefix), ng, blockIdx.x, gridDim.x);
+    const PagedStart* starts = reinterpret_cast<const PagedStart*>(p.ws + L.starts);
+    const PagedGroup* groups = reinterpret_cast<const PagedGroup*>(p.ws + L.groups);
+    const bool work = paged_share_begin(share, starts, blockIdx.x);
 
     if (!work) {
         // nothing in flight: straight to the end
-        if (tid == 0) reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = PagedNote{};
     } else if (warp < 4) {
       regs_dec<PcShape<FP8>::control>();
       if (warp == 0 || warp == 3) {
@@ -440,22 +518,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t tile = sbase + (is_k ? kPcK : kPcV);
         uint32_t qph[2] = {0u, 0u}, st = 0, ph = 0, narm_q[2] = {0u, 0u}, narm = 0;
         bool ok = true;
-        for (; ok && paged_share_next(share, sg, first); first = false) {
+        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
-            if (!is_k && first && lane == 0) {
-                // a pair that the share begins inside of is held in part by the
-                // CTAs before, too: the first CTA of those leaves the combine a note
-                const long long W = hdr->chunk.tiles * ng, G = W < (long long)gridDim.x ? W : (long long)gridDim.x;
-                PagedNote n = {};
-                if (sg.t0 > 0) {
-                    n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.g.tiles);
-                    n.fold = n.parts.cf == (int)blockIdx.x - 1;
-                    n.row = sg.g.row;
-                    n.head = sg.head;
-                    n.rows = kGroup * sg.g.nrows;
-                }
-                reinterpret_cast<PagedNote*>(p.ws + L.notes)[blockIdx.x] = n;
-            }
             const int ntile = !is_k ? 0 : sg.g.nrows > kTokPerTile ? 2 : 1;
             for (int t = 0; t < ntile && ok; ++t) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_Q_EMPTY + t), qph[t] ^ 1, abort_flag, status));
@@ -542,7 +606,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // lane 0 waits and issues, the others follow its outcome
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qrph[2] = {0u, 0u}, pph[2] = {0u, 0u};
         bool ok = true;
-        for (; ok && paged_share_next(share, sg, first); first = false) {
+        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
             if (lane == 0) {
                 const PcGroup gr = pc_group(p, sg.g);
                 const int ntile = sg.g.nrows > kTokPerTile ? 2 : 1, n = sg.t1 - sg.t0;
@@ -607,7 +671,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ============================================================ V rows without a position
         uint32_t st = 0, ph = 0;
         bool ok = true;
-        for (; ok && paged_share_next(share, sg, first); first = false) {
+        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
             const PcGroup gr = pc_group(p, sg.g);
             for (int ch = sg.t0; ch < sg.t1; ++ch) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_FULL + st), ph, abort_flag, status));
@@ -644,7 +708,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint8_t* vp = static_cast<const uint8_t*>(p.v_pages);
         uint32_t st = 0, ph = 0;
         bool ok = true;
-        for (; ok && paged_share_next(share, sg, first); first = false) {
+        // the place in the share is kept in shared memory: the codes on their
+        // way take the registers
+        PagedShare* walk = reinterpret_cast<PagedShare*>(smem + kPcWalk) + w;
+        if (lane == 0) *walk = share;
+        __syncwarp();
+        auto next_pair = [&]() -> bool {
+            PagedShare sh = *walk;
+            __syncwarp();
+            const bool more = paged_share_next(sh, groups, ng, sg, false);
+            if (lane == 0) *walk = sh;
+            __syncwarp();
+            return more;
+        };
+        while (ok && next_pair()) {
             const PcGroup gr = pc_group(p, sg.g);
             const int* table = c.table + (size_t)sg.g.b * c.max_pages;
             // Pages of the warp's 32 positions of chunk ch, lane l's position
@@ -747,7 +824,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // whole and first.
         struct Work { int ks, n, hi, pos0, row, info; };
         auto fetch = [&](Work& w) -> bool {
-            while (paged_share_next(share, sg, first)) {
+            while (paged_share_next(share, groups, ng, sg, first)) {
                 const bool f = first;
                 first = false;
                 if (t != 0 && sg.g.nrows <= kTokPerTile) continue;

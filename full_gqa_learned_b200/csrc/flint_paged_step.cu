@@ -977,7 +977,6 @@ cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStre
 }
 
 // The workspace does not depend on the device: room for a full B200's CTAs.
-constexpr int kPagedMaxSms = 148;
 
 // Calls whose sequences all have at most this many new tokens run the step
 // kernel, others the chunk kernel: the step kernel reads a sequence's keys and

@@ -190,6 +190,28 @@ def test_chunks(fa, ps, fp8, ctx, new, window):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("where", [0, 60, 200])
+def test_chunks_of_unlike_pairs(fa, fp8, where):
+    """One long sequence among 200 whose pairs have a chunk or two: where a
+    CTA's share begins goes by a pair's cost, not by its chunks alone."""
+    r = np.random.default_rng(31)
+    ctx, new = r.integers(0, 140, 200).tolist(), r.integers(0, 4, 200).tolist()
+    ctx.insert(where, 9001)
+    new.insert(where, 40)
+    c = Case(ctx, new, ps=32, fp8=fp8, seed=32)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, out, lse = attend(fa, c, t)
+    assert st == 0
+    check_attend(c, t, out, lse, chunk=True)
+    if fp8:                                               # converted on chip
+        least = fa.paged_workspace_bytes(c.B, c.T, 40, c.table.shape[1], 32, window=0)
+        st, out, lse = attend(fa, c, t, workspace=torch.empty(least, dtype=torch.uint8, device="cuda"))
+        assert st == 0
+        check_attend(c, t, out, lse, chunk=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_far_positions_and_extreme_sinks(fa, fp8):
     sinks = np.array([np.inf, -np.inf, 80.0, -80.0] * 8, np.float32)
     c = Case([262100, 1 << 20, 12], [1, 2, 1], ps=32, fp8=fp8, window=129, rope=True, seed=6, sinks=sinks)
