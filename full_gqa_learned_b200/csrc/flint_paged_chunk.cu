@@ -181,11 +181,16 @@ __device__ __forceinline__ int plan_new(const PagedAttnParams& p, int b, bool* b
 // sequences only every `every`-th is, and the rest is walked.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 4096;
-// A chunk takes about 3 us, a pair's query prologue and epilogue 5 to 6.  24
-// sequences with 1 to 384 new tokens, window 513 (2,049), over up to 40,000
-// positions of 16-bit pages: shares by chunks alone 139 us (330), pairs as 1
-// chunk 130 (287), as 1.5 122 (281), as 2 125 (279), as 4 131 (270).
+// A chunk takes about 3 us, a pair's query prologue and epilogue 5 to 6; a pair
+// held in part costs both again, 128 KiB of partial results and the combine, so
+// a boundary near a pair's end moves there: within a chunk, or with two pairs a
+// CTA or more a 16th of a share, at most 4 chunks.  24 sequences with 1 to 384
+// new tokens over up to 40,000 positions: window 513, 8-bit (2,049, 16-bit):
+// shares by chunks alone 160 us (331), by chunks and pairs 146 (281), moved by
+// a chunk 123 (270), by the rule 123 (257); twice the sequences 260 -> 232.  Where
+// there are 1.3 pairs of 33 chunks a CTA, moving by 2 costs 4 us of 257.
 constexpr long long kCostChunk = 2, kCostPair = 3;
+constexpr int kSnapPart = 16, kSnapMost = 4;
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAttnParams p) {
     griddep_launch_dependents();
     __shared__ int s_bad, sh_i[32], off[kPlanSeqs];
@@ -270,12 +275,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
         hdr->status = s_bad ? kStatusInvalid : kStatusOk;
     }
     __syncthreads();
-    // Where the CTAs start.  A pair costs its chunks and its prologue and
-    // epilogue; where a share is too short for every CTA to get a chunk that
-    // way, chunks alone count.
+    // Where the CTAs start.  Where shares are too short for every CTA to get a
+    // chunk by the rule above, chunks alone count (a constant start takes at
+    // most (2 snap + 1) a + o of the cost).
     const long long all = tiles * c.ng;
     long long W = c.ng * (kCostChunk * tiles + kCostPair * n_groups), a = kCostChunk, o = kCostPair, G = p.chunk_ctas;
-    if (W / G < a + o) {
+    int snap = (long long)n_groups * c.ng < 2 * G ? 1 : max(1, min(kSnapMost, (int)(all / (kSnapPart * G))));
+    if (W / G < (2 * snap + 2) * a + 2 * o) {
+        snap = 0;
         W = all;
         a = 1;
         o = 0;
@@ -293,7 +300,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedAtt
             }
             const long long g0 = pre(lo), k = pre(lo + 1) - g0, in = pos - c.ng * (a * g0 + o * lo), w = a * k + o;
             const int head = (int)(in / w);
-            const long long off = max(in - head * w - o + a - 1, 0ll) / a;       // a chunk belongs to whose share holds its first unit
+            long long off = max(in - head * w - o + a - 1, 0ll) / a;             // a chunk belongs to whose share holds its first unit
+            off = off <= snap ? 0 : k - off <= snap ? k : off;
             st.x = g0 * c.ng + head * k + off;
             st.gi = lo;
             st.head = head;
