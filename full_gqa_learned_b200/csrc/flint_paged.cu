@@ -288,6 +288,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadPar
     const long long t0 = (long long)(blockIdx.x * (kPagedThreads >> 5) + warp) * per;
     if (t0 < p.c.T) {
       const PagedPlace place = paged_locate(p.c, (int)t0, per);
+      const bool wide = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 31) == 0;
       // four passes' loads on their way at once
       for (int i0 = 0; i0 < per; i0 += 4 * kTok) {
         uint4 ka[4], kb[4], va[4], vb[4];
@@ -338,8 +339,15 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadPar
                 }
                 uint4* kd = reinterpret_cast<uint4*>(p.k + r * kHD + 16 * sub);
                 uint4* vd = reinterpret_cast<uint4*>(p.v + r * kHD + 16 * sub);
-                kd[0] = *reinterpret_cast<uint4*>(&ko[0]); kd[1] = *reinterpret_cast<uint4*>(&ko[4]);
-                vd[0] = *reinterpret_cast<uint4*>(&vo[0]); vd[1] = *reinterpret_cast<uint4*>(&vo[4]);
+                const uint4 k0 = *reinterpret_cast<uint4*>(&ko[0]), k1 = *reinterpret_cast<uint4*>(&ko[4]);
+                const uint4 v0 = *reinterpret_cast<uint4*>(&vo[0]), v1 = *reinterpret_cast<uint4*>(&vo[4]);
+                if (wide) {
+                    st_32(kd, k0, k1);
+                    st_32(vd, v0, v1);
+                } else {
+                    kd[0] = k0; kd[1] = k1;
+                    vd[0] = v0; vd[1] = v1;
+                }
             }
         }
       }

@@ -163,6 +163,12 @@ __device__ __forceinline__ PagedParts paged_parts(long long W, long long G, long
     return r;
 }
 
+// 32 bytes by one store (p 32-byte aligned): two of 16 leave half a sector each.
+__device__ __forceinline__ void st_32(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+}
+
 // What a CTA leaves for the kernel that folds the parts.
 struct PagedNote {
     int status;                  // the CTA's (step kernel)

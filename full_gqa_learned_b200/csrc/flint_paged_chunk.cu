@@ -403,12 +403,8 @@ __global__ void __launch_bounds__(kExpandThreads) paged_expand_kernel(const Page
                 ko[e] = *reinterpret_cast<const uint32_t*>(&kk);
                 vo[e] = pc_pack_bf16(vf.x * vsf, vf.y * vsf);
             }
-            uint4* kd = reinterpret_cast<uint4*>(ks + (dst + r) * kHD + 16 * sub);
-            uint4* vd = reinterpret_cast<uint4*>(vs + (dst + r) * kHD + 16 * sub);
-            kd[0] = make_uint4(ko[0], ko[1], ko[2], ko[3]);
-            kd[1] = make_uint4(ko[4], ko[5], ko[6], ko[7]);
-            vd[0] = make_uint4(vo[0], vo[1], vo[2], vo[3]);
-            vd[1] = make_uint4(vo[4], vo[5], vo[6], vo[7]);
+            st_32(ks + (dst + r) * kHD + 16 * sub, make_uint4(ko[0], ko[1], ko[2], ko[3]), make_uint4(ko[4], ko[5], ko[6], ko[7]));
+            st_32(vs + (dst + r) * kHD + 16 * sub, make_uint4(vo[0], vo[1], vo[2], vo[3]), make_uint4(vo[4], vo[5], vo[6], vo[7]));
         }
     }
     // nothing above needs the plan; it writes the status word, and who waits
