@@ -6,16 +6,17 @@
 // "flint.layers" API page; weight-form RMSNorm, then NeoX RoPE on sliding
 // layers), in FP32 with one rounding at the end, and goes with its value to
 // the slot the page table names.  8-bit pages: with a the row's largest
-// magnitude, e is the smallest integer in [-24, 40] with a <= 448 x 2^e (448:
-// the largest E4M3 number), the codes are E4M3(x 2^-e).  A power of two makes
+// magnitude, e is the smallest integer in [-24, 40] (keys: to 7, so that FP16
+// holds them) with a <= 448 x 2^e (448: the largest E4M3 number), the codes are
+// E4M3(x 2^-e).  A power of two makes
 // the scaling exact, so the code's rounding (half a step, 2^-4 relative) is
 // the only one, and what is read back is exact in FP16 or BF16.  An arbitrary
 // scale would not round better: E4M3 is a floating format.
 //
 // Both kernels move bytes: 512 read and 512 or 258 written per token and head
 // (append), the reverse for reading.  Measured (launch included): appending
-// 21,455 tokens to 8-bit pages 18 us (3.6 TB/s), reading 103,592 back 78 us
-// (4.1 TB/s; a copy of as many bytes 50); 128 tokens, or 4,096 read, 8 us, which
+// 21,455 tokens to 8-bit pages 18 us (3.6 TB/s), reading 103,592 back 57 us
+// (5.6 TB/s; a copy of as many bytes 50); 128 tokens, or 4,096 read, 8 us, which
 // is launch and four dependent loads.
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -44,10 +45,10 @@ __device__ void paged_check_block(const PagedCache& c, int* status, bool keep_no
     // threads per sequence: a power of two, so that the entries of few long
     // sequences and those of many short ones are both read in parallel
     int per = 1;
-    while (per < 32 && c.B * per * 2 <= kPagedThreads) per *= 2;
+    while (per < 32 && c.B * per * 2 <= (int)blockDim.x) per *= 2;
     const int sub = threadIdx.x % per;
     if (threadIdx.x == 0 && (c.cu[0] != 0 || c.cu[c.B] > c.T)) bad = true;
-    for (int b = threadIdx.x / per; b < c.B; b += kPagedThreads / per) {
+    for (int b = threadIdx.x / per; b < c.B; b += blockDim.x / per) {
         const int a = c.cu[b], n = c.cu[b + 1] - a, L = c.len[b];
         if (a < 0 || n < 0 || n > c.T || L < 0 || L >= FLINT_MAX_TOKENS) { bad = true; continue; }
         if (n == 0) continue;
@@ -95,11 +96,16 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedCache& c, int t0, 
 }
 
 // Tokens a warp takes: eight on long calls, so that one look-up serves many
-// rows and many loads are on their way; fewer where a call of few tokens would
-// leave SMs idle.  Measured (launch included): reading 103,592 tokens of 8-bit
-// pages 88 us with one token a warp, 76 with eight; appending 21,455 is the
-// same 20 us either way.
+// rows; fewer where a call of few tokens would leave SMs idle.  Measured:
+// appending 78,523 tokens to 8-bit (16-bit) pages 49 us (55), with 16 tokens a warp
+// 55 (59).
 __host__ __device__ inline int paged_tokens_per_warp(int T) { return T >= 16384 ? 8 : T >= 4096 ? 4 : T >= 2048 ? 2 : 1; }
+// Reading, the longest calls take 32: fewer rows on their way at once keep the
+// memory's reads and writes in longer runs (more resident blocks or smaller ones
+// are slower, too).  Measured: 103,592 tokens of 8-bit (16-bit) pages 57 us (74),
+// with 8 tokens a warp 70 (82); 42,772 tokens 26 (31), with 32 33 (35).
+constexpr int kReadThreads = 256;
+__host__ __device__ inline int paged_read_tokens(int T) { return T >= 65536 ? 32 : paged_tokens_per_warp(T); }
 
 // E8M0 exponent e of a row whose largest magnitude is a.
 __device__ __forceinline__ int paged_exponent(float a, int most) {
@@ -134,7 +140,7 @@ struct AppendParams {
 
 template <int NG, bool FP8>
 __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const AppendParams p) {
-    if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.x == 0) {                             // first, so that no wave of the others is before it
         paged_check_block(p.c, p.status, true);
         return;
     }
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
     // a pass: 4 / NG tokens, four rows of eight lanes
     constexpr int kTok = 4 / NG;
     const int per = max(kTok, paged_tokens_per_warp(p.c.T));
-    const long long t0 = (long long)(blockIdx.x * (kPagedThreads >> 5) + warp) * per;
+    const long long t0 = (long long)((blockIdx.x - 1) * (kPagedThreads >> 5) + warp) * per;
     if (t0 < p.c.T) {
       const PagedPlace place = paged_locate(p.c, (int)t0, per);
 #pragma unroll 2
@@ -276,16 +282,16 @@ __device__ __forceinline__ float2 paged_decode2(uint32_t codes) {
 }
 
 template <int NG, bool FP8>
-__global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const ReadParams p) {
-    if (blockIdx.x == gridDim.x - 1) {
+__global__ void __launch_bounds__(kReadThreads) paged_read_kernel(const ReadParams p) {
+    if (blockIdx.x == 0) {
         paged_check_block(p.c, p.status, false);
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int grp = lane >> 3, sub = lane & 7;
     constexpr int kTok = 4 / NG;
-    const int per = max(kTok, paged_tokens_per_warp(p.c.T));
-    const long long t0 = (long long)(blockIdx.x * (kPagedThreads >> 5) + warp) * per;
+    const int per = max(kTok, paged_read_tokens(p.c.T));
+    const long long t0 = (long long)((blockIdx.x - 1) * (kReadThreads >> 5) + warp) * per;
     if (t0 < p.c.T) {
       const PagedPlace place = paged_locate(p.c, (int)t0, per);
       const bool wide = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 31) == 0;
@@ -420,13 +426,12 @@ flint_status_t check_workspace(const void* workspace, size_t have, size_t need) 
     return FLINT_OK;
 }
 
-// Blocks of the row kernels: a warp per paged_tokens_per_warp tokens (and at
-// least four rows), and the checking block.
-int row_blocks(const PagedCache& c) {
-    int per = paged_tokens_per_warp(c.T);
+// Blocks of a row kernel whose warps take per tokens (at least four rows), and
+// the checking block.
+int row_blocks(const PagedCache& c, int per, int threads) {
     if (per < 4 / c.ng) per = 4 / c.ng;
     const long long warps = ((long long)c.T + per - 1) / per;
-    return (int)((warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32)) + 1;
+    return (int)((warps + threads / 32 - 1) / (threads / 32)) + 1;
 }
 
 template <bool FP8>
@@ -437,9 +442,9 @@ void launch_append(const AppendParams& p, int grid, cudaStream_t s) {
 }
 template <bool FP8>
 void launch_read(const ReadParams& p, int grid, cudaStream_t s) {
-    if (p.c.ng == 4) paged_read_kernel<4, FP8><<<grid, kPagedThreads, 0, s>>>(p);
-    else if (p.c.ng == 2) paged_read_kernel<2, FP8><<<grid, kPagedThreads, 0, s>>>(p);
-    else paged_read_kernel<1, FP8><<<grid, kPagedThreads, 0, s>>>(p);
+    if (p.c.ng == 4) paged_read_kernel<4, FP8><<<grid, kReadThreads, 0, s>>>(p);
+    else if (p.c.ng == 2) paged_read_kernel<2, FP8><<<grid, kReadThreads, 0, s>>>(p);
+    else paged_read_kernel<1, FP8><<<grid, kReadThreads, 0, s>>>(p);
 }
 
 }  // namespace
@@ -480,7 +485,7 @@ flint_status_t flint_paged_append(const void* k, const void* v, const float* k_n
     p.use_rope = use_rope;
     p.rope_theta = rope_theta;
     p.eps = eps;
-    const int grid = row_blocks(p.c);
+    const int grid = row_blocks(p.c, paged_tokens_per_warp(p.c.T), kPagedThreads);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (k_scales) launch_append<true>(p, grid, s);
     else launch_append<false>(p, grid, s);
@@ -513,7 +518,7 @@ flint_status_t flint_paged_read(const void* k_pages, const void* v_pages, const 
     p.k = static_cast<__half*>(k);
     p.v = static_cast<__nv_bfloat16*>(v);
     p.status = static_cast<int*>(workspace);
-    const int grid = row_blocks(p.c);
+    const int grid = row_blocks(p.c, paged_read_tokens(p.c.T), kReadThreads);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (k_scales) launch_read<true>(p, grid, s);
     else launch_read<false>(p, grid, s);
