@@ -214,14 +214,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const Appen
         const size_t row = ok ? paged_row(p.c, page, head, pos & ((1 << p.c.ps_log2) - 1)) : 0;
         if constexpr (!FP8) {
             if (ok) {
+                // |k~| <= sqrt(128) max|w|: only weights above 5,789 reach the clamp; NaN stays
+                const __half2 top = __float2half2_rn(65504.f), low = __float2half2_rn(-65504.f);
                 __half2 h[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    // |k~| <= sqrt(128) max|w|: only weights above 5,789 reach the clamp
-                    h[e] = __floats2half2_rn(fminf(fmaxf(x0[2 * e], -65504.f), 65504.f),
-                                             fminf(fmaxf(x0[2 * e + 1], -65504.f), 65504.f));
-                    h[4 + e] = __floats2half2_rn(fminf(fmaxf(x1[2 * e], -65504.f), 65504.f),
-                                                 fminf(fmaxf(x1[2 * e + 1], -65504.f), 65504.f));
+                    h[e] = __hmin2_nan(__hmax2_nan(__floats2half2_rn(x0[2 * e], x0[2 * e + 1]), low), top);
+                    h[4 + e] = __hmin2_nan(__hmax2_nan(__floats2half2_rn(x1[2 * e], x1[2 * e + 1]), low), top);
                 }
                 __half* kd = static_cast<__half*>(p.k_pages) + row * kHD + 8 * sub;
                 __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(p.v_pages) + row * kHD + 8 * sub;

@@ -339,6 +339,30 @@ def test_keys_saturate_within_fp16(fa):  # noqa: F811
         assert torch.isfinite(k).all() and k.abs().max().item() == top
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1, 1], [20, 3]])
+def test_nan_of_a_token_is_not_hidden(fa, fp8, new):  # noqa: F811
+    """A NaN in a key or value stays one in the pages and in the outputs that
+    see it; other sequences and heads do not."""
+    c = Case([40, 18], new, fp8=fp8, ps=16, seed=33)
+    t = c.to("cuda")
+    t["k"][0, 1, 5] = float("nan")
+    t["v"][0, 2, 7] = float("nan")
+    assert append(fa, c, t) == 0
+    page, slot = c.slots()
+    K, V = values(t["k_pages"], t["k_scales"]), values(t["v_pages"], t["v_scales"])
+    assert np.isnan(K[page[0], 1, slot[0]]).all()          # the whole row: its norm is NaN
+    assert np.isnan(V[page[0], 2, slot[0], 7]) and np.isnan(V[page[0], 2, slot[0]]).sum() == 1
+    assert not np.isnan(K[page[0], [0, 2, 3], slot[0]]).any()
+    st, out, _ = attend(fa, c, t)
+    assert st == 0
+    out = out.float().reshape(c.T, 32, 128).cpu()
+    n = new[0]
+    assert torch.isnan(out[:n, 8:16]).all() and torch.isnan(out[:n, 16:24, 7]).all()
+    assert not torch.isnan(out[:n, 16:24, :7]).any() and not torch.isnan(out[:n, :8]).any() and not torch.isnan(out[:n, 24:]).any()
+    assert not torch.isnan(out[n:]).any()
+
+
 def test_offsets_past_32_bits(fa):  # noqa: F811
     """A pool of over 2^31 elements: the pages in use are its last ones."""
     c = Case([300, 65], [2, 1], ps=128, seed=25)
