@@ -304,7 +304,9 @@ def _paged_stream(stream, dev):
     ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if ptr == current:
         return current, None
-    return ptr, torch.cuda.ExternalStream(ptr, device=dev)
+    if hasattr(stream, "cuda_stream"):
+        return ptr, stream
+    return ptr, torch.cuda.ExternalStream(ptr, device=dev) if ptr else torch.cuda.default_stream(dev)
 
 
 def _paged_new(like, shape, dtype, side):

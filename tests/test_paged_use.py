@@ -177,6 +177,21 @@ def test_another_stream_gets_its_own_memory(fa):  # noqa: F811
     assert torch.equal(read[0], wk) and torch.equal(read[1], wv)
 
 
+def test_default_stream_from_a_side_stream(fa):  # noqa: F811
+    """The default stream by object and by number, while another is current."""
+    c = Case([70, 9], [2, 1], seed=34)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    _, want, wl = attend(fa, c, t)
+    args = [t[n] for n in ("q", "wq", "sinks", "k_pages", "v_pages", "table", "ctx", "cu")]
+    torch.cuda.synchronize()
+    for stream in (0, torch.cuda.default_stream()):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out, lse = fa.attn_paged(*args, max_new=2, window=0, use_rope=False, stream=stream)
+        assert fa.device_status(fa.attn_paged.last_workspace, stream) == 0
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 @pytest.mark.parametrize("given", [False, True])
 def test_empty_calls_have_a_status(fa, given):  # noqa: F811
     """No sequences, or no tokens: nothing is launched, and the status is not
