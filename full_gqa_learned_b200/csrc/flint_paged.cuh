@@ -243,9 +243,8 @@ struct PagedShare {
 };
 struct PagedSeg {
     PagedGroup g;
-    int gi, head, t0, t1;        // tiles [t0, t1) of pair (gi, head)
+    int head, t0, t1;            // tiles [t0, t1) of the group's pair with this head
     bool whole;                  // all of it
-    bool first;                  // the share's first pair
 };
 __device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedStart* starts, int cta) {
     const PagedStart at = starts[cta];
@@ -255,15 +254,13 @@ __device__ __forceinline__ bool paged_share_begin(PagedShare& s, const PagedStar
     s.left = (int)(starts[cta + 1].x - at.x);
     return s.left > 0;
 }
-__device__ __forceinline__ bool paged_share_next(PagedShare& s, const PagedGroup* groups, int ng, PagedSeg& g, bool first) {
+__device__ __forceinline__ bool paged_share_next(PagedShare& s, const PagedGroup* groups, int ng, PagedSeg& g) {
     if (s.left <= 0) return false;
     g.g = groups[s.gi];
-    g.gi = s.gi;
     g.head = s.head;
     g.t0 = s.off;
     g.t1 = min(g.g.tiles, s.off + s.left);
     g.whole = g.t0 == 0 && g.t1 == g.g.tiles;
-    g.first = first;
     s.left -= g.t1 - g.t0;
     s.off = 0;
     if (++s.head == ng) { s.head = 0; ++s.gi; }

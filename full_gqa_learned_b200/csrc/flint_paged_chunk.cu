@@ -522,7 +522,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t tile = sbase + (is_k ? kPcK : kPcV);
         uint32_t qph[2] = {0u, 0u}, st = 0, ph = 0, narm_q[2] = {0u, 0u}, narm = 0;
         bool ok = true;
-        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
+        while (ok && paged_share_next(share, groups, ng, sg)) {
             const PcGroup gr = pc_group(p, sg.g);
             const int ntile = !is_k ? 0 : sg.g.nrows > kTokPerTile ? 2 : 1;
             for (int t = 0; t < ntile && ok; ++t) {
@@ -610,7 +610,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // lane 0 waits and issues, the others follow its outcome
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qrph[2] = {0u, 0u}, pph[2] = {0u, 0u};
         bool ok = true;
-        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
+        while (ok && paged_share_next(share, groups, ng, sg)) {
             if (lane == 0) {
                 const PcGroup gr = pc_group(p, sg.g);
                 const int ntile = sg.g.nrows > kTokPerTile ? 2 : 1, n = sg.t1 - sg.t0;
@@ -675,7 +675,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // ============================================================ V rows without a position
         uint32_t st = 0, ph = 0;
         bool ok = true;
-        for (; ok && paged_share_next(share, groups, ng, sg, first); first = false) {
+        while (ok && paged_share_next(share, groups, ng, sg)) {
             const PcGroup gr = pc_group(p, sg.g);
             for (int ch = sg.t0; ch < sg.t1; ++ch) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(PC_V_FULL + st), ph, abort_flag, status));
@@ -720,7 +720,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         auto next_pair = [&]() -> bool {
             PagedShare sh = *walk;
             __syncwarp();
-            const bool more = paged_share_next(sh, groups, ng, sg, false);
+            const bool more = paged_share_next(sh, groups, ng, sg);
             if (lane == 0) *walk = sh;
             __syncwarp();
             return more;
@@ -828,7 +828,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // whole and first.
         struct Work { int ks, n, hi, pos0, row, info; };
         auto fetch = [&](Work& w) -> bool {
-            while (paged_share_next(share, groups, ng, sg, first)) {
+            while (paged_share_next(share, groups, ng, sg)) {
                 const bool f = first;
                 first = false;
                 if (t != 0 && sg.g.nrows <= kTokPerTile) continue;
