@@ -137,7 +137,9 @@ struct PagedStart {
     int gi, head, off, pad;
 };
 
-constexpr int kPagedMaxSms = 148;        // SMs that a call's shares are cut for
+// SMs that a call's shares are cut for.  The workspace does not depend on the
+// device: room for a full B200's CTAs.
+constexpr int kPagedMaxSms = 148;
 constexpr int kChunkTok = 32;            // new tokens of a chunk kernel's group
 constexpr int kPagedStepRows = 16;       // query rows of a step partial
 // floats of a step partial: m[16], l[16], O[16][128]; of a chunk partial:

@@ -976,21 +976,19 @@ cudaError_t launch_step(const StepMaps& maps, const PagedAttnParams& p, cudaStre
     return cudaLaunchKernelEx(&cfg, paged_fold_kernel, p);
 }
 
-// The workspace does not depend on the device: room for a full B200's CTAs.
-
 // Calls whose sequences all have at most this many new tokens run the step
 // kernel, others the chunk kernel: the step kernel reads a sequence's keys and
 // values once per two tokens, the chunk kernel once per 32 but with more to set
 // up.  Measured, 16 sequences on two heads over 700 to 16,383 positions, step /
-// chunk: 9 tokens 98 / 78 us, 12 117 / 76, 16 150 / 79 (8-bit pages: 9 88 / 113,
-// 16 125 / 114); 25 sequences of 4 to 9 tokens over none 20 / 26.
+// chunk: 9 tokens 98 / 75 us, 12 117 / 73, 16 150 / 75 (8-bit pages: 9 88 / 97,
+// 16 125 / 97); 25 sequences of 4 to 9 tokens over none 20 / 26.
 constexpr int kStepMaxNew = 8;
 
 // Positions a sequence has room for where the chunk kernel's calls on 8-bit
 // pages expand them to 16 bits: the window of its new tokens, from a page's
 // start; 0 where all sequences' would take more than 512 MiB.  Expanding is
 // faster wherever there is room (expanded / on chip: 16 sequences over 700 to
-// 16,383 positions, 9 new tokens each 114 / 134 us, 64 163 / 253, 128 244 / 454);
+// 16,383 positions, 9 new tokens each 97 / 115 us, 64 145 / 226, 128 223 / 424);
 // the limit keeps the workspace from outgrowing the cache it saves.
 int stage_rows(int B, int max_new, int max_pages, int page_size, int ng, int window) {
     long long span = (long long)max_pages * page_size;

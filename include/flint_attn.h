@@ -454,8 +454,8 @@ FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pag
  *             > 8 that counts room (up to 512 MiB, else none) to expand the
  *             positions the call reads to 16 bits first; a workspace of the
  *             size for 16-bit pages (eight_bit == 0) is accepted, too: the
- *             call then converts on chip, with the same result, in about twice
- *             the time.
+ *             call then converts on chip, with the same result, in 1.2 times
+ *             (few tokens a sequence) to twice the time.
  * Cached values and keys at positions a token sees must be finite, keys within
  * FP16's range, and scales within 2^-24 .. 2^40; slots of other positions may hold anything, and page
  * table entries that no new token's window touches are not read.
