@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libflint_attn.so")
 SOURCES = ["flint_abi.cu", "flint_prep.cu", "flint_attn.cu", "flint_static.cu", "flint_decode.cu", "flint_decode_tc.cu",
            "flint_bwd.cu", "flint_bwd_tc.cu", "flint_gemm.cu", "flint_paged.cu", "flint_paged_step.cu",
            "flint_paged_chunk.cu"]
-HEADERS = ["flint_common.cuh", "sm100.cuh", "flint_host.cuh", "flint_decode.cuh", "flint_paged.cuh"]
+HEADERS = ["flint_common.cuh", "sm100.cuh", "flint_host.cuh", "flint_decode.cuh", "flint_paged.cuh",
+           "flint_paged_walk.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -41,21 +41,37 @@ __device__ __forceinline__ size_t paged_row(const PagedCache& c, int page, int g
     return (((size_t)page * c.ng + g) << c.ps_log2) + slot;
 }
 
+// A word of the call's arrays (read-only while its kernels run).
+__host__ __device__ __forceinline__ int paged_ld(const int* p) {
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
+}
+
 // Last b in [0, n) with a[b] <= x, for a non-decreasing a with a[0] <= x;
 // warp-wide (x uniform): 32 probes a step.  Any other a gives some index in
-// [0, n), so callers check what they read there.
+// [0, n), so callers check what they read there.  On the host one thread makes
+// the same probes.
 template <typename I, typename X>
-__device__ __forceinline__ int warp_last_leq(const I* a, int n, X x) {
-    const int lane = threadIdx.x & 31;
+__host__ __device__ __forceinline__ int warp_last_leq(const I* a, int n, X x) {
     int lo = 0;
     while (n > 1) {
         const int step = (n + 31) >> 5;
-        const int at = lane * step;
+        int k = 0;
+#ifdef __CUDA_ARCH__
+        const int at = (int)(threadIdx.x & 31) * step;
         const bool le = at < n && (X)a[lo + at] <= x;
         const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int k = m ? 31 - __clz(m) : 0;
+        if (m) k = 31 - __clz(m);
+#else
+        for (int l = 0; l < 32 && l * step < n; ++l)
+            if ((X)a[lo + l * step] <= x) k = l;
+#endif
         lo += k * step;
-        n = min(step, n - k * step);
+        const int rest = n - k * step;
+        n = step < rest ? step : rest;
     }
     return lo;
 }
@@ -214,10 +230,11 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas,
 
 // New tokens of the sequence whose packed rows are [a, z) at positions len ..;
 // -1 where its entries are ill-formed.
-__device__ __forceinline__ int paged_new(const PagedCache& c, int max_new, int a, int z, int len) {
+__host__ __device__ __forceinline__ int paged_new(const PagedCache& c, int max_new, int a, int z, int len) {
+    if (a < 0 || z < a || z > c.T || len < 0 || len >= FLINT_MAX_TOKENS) return -1;
     const int n = z - a;
-    if (a < 0 || z < a || z > c.T || n > max_new || len < 0 || len >= FLINT_MAX_TOKENS) return -1;
     const long long end = (long long)len + n;
+    if (n > max_new) return -1;
     return n > 0 && (end > FLINT_MAX_TOKENS || end > ((long long)c.max_pages << c.ps_log2)) ? -1 : n;
 }
 

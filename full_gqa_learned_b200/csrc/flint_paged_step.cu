@@ -61,7 +61,7 @@
 #include <cuda_runtime.h>
 
 #include "flint_host.cuh"
-#include "flint_paged.cuh"
+#include "flint_paged_walk.cuh"
 #include "sm100.cuh"
 
 namespace flint {
@@ -149,81 +149,10 @@ struct StepSmem {
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
 enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6 };
 
-// A walk over a share of the step's work: the pairs (row group, KV head),
-// sequence by sequence, group by group, head by head.
-struct StepWalk {
-    int b, a, n, len;            // the sequence, its first packed row, new tokens, cached positions
-    int z1, len1;                // the next sequence's end and cached positions, on their way
-    int row0, head, off, left;   // next pair: first row, head, tile it is entered at; tiles left in the share
-};
-struct StepSeg {
-    int b, head, p0, row, nrows, tiles, t0, t1;
-    bool whole, first;
-};
-// Tiles start at a multiple of the box: min(page, tile).
-__device__ __forceinline__ int step_base(const PagedAttnParams& p, int lo, int tile) {
-    return lo & ~(min(1 << p.c.ps_log2, tile) - 1);
-}
-__device__ __forceinline__ int step_tiles(const PagedAttnParams& p, int p0, int nrows, int tile) {
-    const int lo = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-    return (p0 + nrows - step_base(p, lo, tile) + tile - 1) / tile;
-}
-// Enters sequence b (rows [a, z), cached positions len), or the next one with
-// new tokens; the whole warp calls it.  Runs of empty sequences are skipped by
-// one search: their boundaries are all z.
-__device__ __forceinline__ void step_enter(const PagedAttnParams& p, StepWalk& w, int b, int a, int z, int len) {
-    const PagedCache& c = p.c;
-    for (;;) {
-        const int n = paged_new(c, p.max_new, a, z, len);
-        w.b = b;
-        w.a = a;
-        w.n = n;
-        w.len = len;
-        const bool more = b + 1 < c.B;
-        w.z1 = more ? __ldg(c.cu + b + 2) : 0;
-        w.len1 = more ? __ldg(c.len + b + 1) : 0;
-        if (n > 0 || !more) return;
-        a = z;
-        ++b;
-        if (w.z1 > a) {
-            z = w.z1;
-            len = w.len1;
-        } else {
-            b += warp_last_leq(c.cu + b, c.B - b, a);
-            a = __ldg(c.cu + b);
-            z = __ldg(c.cu + b + 1);
-            len = __ldg(c.len + b);
-        }
-    }
-}
-template <int NT>
-__device__ __forceinline__ bool step_next(const PagedAttnParams& p, StepWalk& w, StepSeg& s, int tile) {
-    if (w.left <= 0) return false;
-    s.b = w.b;
-    s.head = w.head;
-    s.p0 = w.len + w.row0;
-    s.row = w.a + w.row0;
-    s.nrows = min(NT, w.n - w.row0);
-    s.tiles = step_tiles(p, s.p0, s.nrows, tile);
-    s.t0 = w.off;
-    s.t1 = min(s.tiles, w.off + w.left);
-    s.whole = s.t0 == 0 && s.t1 == s.tiles;
-    w.left -= s.t1 - s.t0;
-    w.off = 0;
-    if (++w.head == p.c.ng) {
-        w.head = 0;
-        w.row0 += NT;
-        if (w.row0 >= w.n) {
-            w.row0 = 0;
-            if (w.left > 0) step_enter(p, w, w.b + 1, __ldg(p.c.cu + w.b + 1), w.z1, w.len1);
-        }
-    }
-    return true;
-}
 // The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
 // share them; *bad: ill-formed boundaries or lengths.  Every thread of the
 // block calls it; false: no share.
-struct StepPlanSmem { long long scan[8]; int at[5]; int bad; };
+struct StepPlanSmem { long long scan[8]; int at[4]; };
 template <int NT>
 __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas, StepPlanSmem* sm, StepWalk& w, long long* W,
                           long long* G, bool* bad) {
@@ -235,13 +164,11 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     bool ill = false;
     long long sum = 0;
     if (b0 < b1) {
-        int a = __ldg(c.cu + b0);
+        int a = paged_ld(c.cu + b0);
         if (b0 == 0) ill = a != 0;
         for (int b = b0; b < b1; ++b) {
-            const int len = __ldg(c.len + b), z = __ldg(c.cu + b + 1);
-            const int n = paged_new(c, p.max_new, a, z, len);
-            ill = ill || n < 0;                               // a last boundary past T as well
-            for (int r = 0; r < n; r += NT) sum += step_tiles(p, len + r, min(NT, n - r), tile);
+            const int len = paged_ld(c.len + b), z = paged_ld(c.cu + b + 1);
+            sum += step_seq_tiles<NT>(p, a, z, len, tile, &ill);   // a last boundary past T as well
             a = z;
         }
     }
@@ -265,33 +192,10 @@ __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas,
     const long long t = *W * cta / *G, end = *W * (cta + 1) / *G;
     if (t >= before * c.ng && t < (before + sum) * c.ng) {
         // the share begins in this thread's run
-        long long in = t - before * c.ng;
-        for (int b = b0; b < b1; ++b) {
-            const int len = __ldg(c.len + b), a = __ldg(c.cu + b), z = __ldg(c.cu + b + 1);
-            const int n = paged_new(c, p.max_new, a, z, len);
-            int r = 0;
-            long long tl = 0;
-            for (; r < n; r += NT) {
-                tl = step_tiles(p, len + r, min(NT, n - r), tile);
-                if (in < tl * c.ng) break;
-                in -= tl * c.ng;
-            }
-            if (r < n) {
-                sm->at[0] = b;
-                sm->at[1] = r;
-                sm->at[2] = (int)(in / tl);
-                sm->at[3] = (int)(in % tl);
-                break;
-            }
-        }
+        step_place<NT>(p, b0, b1, t - before * c.ng, tile, sm->at);
     }
     __syncthreads();
-    const int b = sm->at[0];
-    step_enter(p, w, b, __ldg(c.cu + b), __ldg(c.cu + b + 1), __ldg(c.len + b));
-    w.row0 = sm->at[1];
-    w.head = sm->at[2];
-    w.off = sm->at[3];
-    w.left = (int)(end - t);
+    step_begin(p, w, sm->at, (int)(end - t), *bad);
     return true;
 }
 
