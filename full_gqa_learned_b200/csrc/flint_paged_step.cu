@@ -129,6 +129,7 @@ __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t reg4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+struct StepPlanSmem { long long scan[8]; int at[4]; };
 template <int NT>
 struct StepSmem {
     static constexpr int rows = 8 * NT;
@@ -136,6 +137,7 @@ struct StepSmem {
     static constexpr uint32_t scales = kStepStages * kStepStage;                       // 8 pieces x (K, V) x 16 bytes a stage
     static constexpr uint32_t q = scales + kStepStages * 256;                          // q~ in FP16
     static constexpr uint32_t ml = q + rows * kHD * 2;                                 // [warp][rows] m, then l
+    static constexpr uint32_t plan = ml;                                               // the plan's, before the pairs
     static constexpr uint32_t fin = ml + 2 * kStepWarps * rows * 4;                    // [rows] output scale
     static constexpr uint32_t inv = (fin + rows * 4 + 15) / 16 * 16;                   // rotation frequencies
     static constexpr uint32_t w = inv + 64 * 8;                                        // q_norm weight
@@ -145,6 +147,8 @@ struct StepSmem {
     static constexpr uint32_t total = misc + 16 + 1024;                                // and alignment slack
     // the warps' parts of a pair meet in the stage read last
     static_assert(kStepWarps * rows * kHD * 4 <= kStepStage, "the warps' outputs fit a stage");
+    static_assert(plan >= kStepStages * kStepStage && plan % 8 == 0 && sizeof(StepPlanSmem) <= fin - plan,
+                  "plain accesses only: the plan stays off what TMA writes");
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
 enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6 };
@@ -152,7 +156,6 @@ enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6 };
 // The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
 // share them; *bad: ill-formed boundaries or lengths.  Every thread of the
 // block calls it; false: no share.
-struct StepPlanSmem { long long scan[8]; int at[4]; };
 template <int NT>
 __device__ bool step_plan(const PagedAttnParams& p, int tile, int cta, int ctas, StepPlanSmem* sm, StepWalk& w, long long* W,
                           long long* G, bool* bad) {
@@ -232,7 +235,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
     StepWalk walk;
     long long W, G;
     bool bad;
-    const bool work = step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem), walk, &W, &G, &bad);
+    const bool work = step_plan<NT>(p, TL::tile, blockIdx.x, gridDim.x, reinterpret_cast<StepPlanSmem*>(smem + S::plan), walk, &W, &G, &bad);
     if (!work) {
         if (tid == 0) *note = PagedNote{bad ? kStatusInvalid : kStatusOk};
         return;
@@ -247,7 +250,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         *s_status = bad ? kStatusInvalid : kStatusOk;
         fence_mbar_init();
     }
-    __syncthreads();                                     // the plan's shared memory becomes the ring
+    __syncthreads();                                     // the barriers are set, the plan's memory is read
     auto see = [&](const StepSeg& g, int* lo, int* hi) {
         *lo = p.window > 0 ? max(0, g.p0 - p.window + 1) : 0;
         *hi = g.p0 + g.nrows;
