@@ -130,12 +130,16 @@ flint_status_t make_map(EncodeTiledFn enc, CUtensorMap* m, CUtensorMapDataType d
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace
+
+namespace flint {
 // Test hook, not part of the ABI.  FLINT_TEST_WAIT_TIMEOUT_MS=n (1..10000),
-// read once when the process first launches the attention kernel, makes that
-// one launch's MMA warps wait n ms on a barrier nothing arrives on, so the
-// bounded-wait timeout path runs; later launches are unaffected.
-std::once_flag g_stall_once;
-std::atomic<unsigned long long> g_stall_ns{0};
+// read once when the process first launches the attention kernel or the paged
+// step kernel, makes that one launch's MMA (consumer) warps wait n ms on a
+// barrier nothing arrives on, so the bounded-wait timeout path runs; later
+// launches are unaffected.
+static std::once_flag g_stall_once;
+static std::atomic<unsigned long long> g_stall_ns{0};
 
 unsigned long long test_stall_once() {
     std::call_once(g_stall_once, [] {
@@ -147,8 +151,7 @@ unsigned long long test_stall_once() {
     if (g_stall_ns.load(std::memory_order_relaxed) == 0) return 0;
     return g_stall_ns.exchange(0);
 }
-
-}  // namespace
+}  // namespace flint
 
 extern "C" {
 

@@ -20,5 +20,8 @@ flint_status_t get_encoder(EncodeTiledFn* fn);
 // Checks for an sm_100 device, sets the attention kernel's shared-memory
 // limit once per device and returns its SM count.
 flint_status_t device_setup(int* sms);
+// Nanoseconds that the timeout test hook makes this launch wait; 0 but for the
+// one launch that FLINT_TEST_WAIT_TIMEOUT_MS asks for.
+unsigned long long test_stall_once();
 
 }  // namespace flint

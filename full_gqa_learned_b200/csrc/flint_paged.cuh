@@ -124,6 +124,9 @@ struct PagedAttnParams {
     int step_ctas, chunk_ctas;   // CTAs of the two kernels (chunk: 0 where it is not run)
     int stage_rows;              // positions a sequence has room to expand to 16 bits (0: none)
     float rope_theta, eps;
+    // > 0: test hook.  The step kernel's consumers first wait this many
+    // nanoseconds on a barrier nothing arrives on (FLINT_ERR_TIMEOUT, abort).
+    unsigned long long test_wait_ns;
 };
 
 // A row group: consecutive new tokens of one sequence that a kernel takes

@@ -142,7 +142,7 @@ struct StepSmem {
     static constexpr uint32_t inv = (fin + rows * 4 + 15) / 16 * 16;                   // rotation frequencies
     static constexpr uint32_t w = inv + 64 * 8;                                        // q_norm weight
     static constexpr uint32_t sink = w + kHD * 4;                                      // the learned sinks
-    static constexpr uint32_t bar = sink + kHQ * 4;                                    // full, empty, consumers
+    static constexpr uint32_t bar = sink + kHQ * 4;                                    // full, empty, consumers, test
     static constexpr uint32_t misc = bar + 8 * 8;                                      // abort flag, CTA status
     static constexpr uint32_t total = misc + 16 + 1024;                                // and alignment slack
     // the warps' parts of a pair meet in the stage read last
@@ -151,7 +151,8 @@ struct StepSmem {
                   "plain accesses only: the plan stays off what TMA writes");
 };
 static_assert(2 * (StepSmem<2>::total + 1024) <= 233472, "two CTAs share an SM");
-enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6 };
+// ST_TEST: nothing arrives here, the timeout test hook waits on it
+enum : uint32_t { ST_FULL = 0, ST_EMPTY = 3, ST_CONS = 6, ST_TEST = 7 };
 
 // The share of CTA `cta` of `ctas`; *W, *G: tiles of all pairs, CTAs that
 // share them; *bad: ill-formed boundaries or lengths.  Every thread of the
@@ -241,11 +242,15 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         return;
     }
     if (tid == 0) {
+        // a whole note first: the fold kernel reads it even where a wait ran
+        // out before the first pair, and the workspace holds anything
+        *note = PagedNote{};
         for (uint32_t x = 0; x < kStepStages; ++x) {
             mbar_init(bar(ST_FULL + x), 1);
             mbar_init(bar(ST_EMPTY + x), kStepWarps);
         }
         mbar_init(bar(ST_CONS), 32 * kStepWarps);
+        mbar_init(bar(ST_TEST), 1);
         *abort_flag = 0;
         *s_status = bad ? kStatusInvalid : kStatusOk;
         fence_mbar_init();
@@ -376,27 +381,20 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
         return ok;
     };
     StepSeg sg;
-    bool alive = csync();
+    bool alive = (p.test_wait_ns == 0 || mbar_wait(bar(ST_TEST), 0, abort_flag, s_status, p.test_wait_ns)) && csync();
     for (bool first = true; alive && step_next<NT>(p, walk, sg, TL::tile); first = false) {
         const int head = sg.head, p0 = sg.p0, nrows = sg.nrows;
         int lo, hi;
         see(sg, &lo, &hi);
-        if (first && tid == 0) {
+        if (first && tid == 0 && sg.t0 > 0) {
             // a pair that the share begins inside of is held in part by the
             // CTAs before, too: the first CTA of those leaves the fold a note
-            PagedNote n = {};
-            if (sg.t0 > 0) {
-                n.parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.tiles);
-                n.fold = n.parts.cf == (int)blockIdx.x - 1;
-                n.row = sg.row;
-                n.head = head;
-                n.rows = kGroup * nrows;
-            }
-            note->fold = n.fold;
-            note->parts = n.parts;
-            note->row = n.row;
-            note->head = n.head;
-            note->rows = n.rows;
+            const PagedParts parts = paged_parts(W, G, W * blockIdx.x / G - sg.t0, sg.tiles);
+            note->fold = parts.cf == (int)blockIdx.x - 1;
+            note->parts = parts;
+            note->row = sg.row;
+            note->head = head;
+            note->rows = kGroup * nrows;
         }
 
         // ---- q~ of the group's rows: warp w takes heads 4 (w % 2) .. + 3 of row w / 2
@@ -927,6 +925,7 @@ flint_status_t launch_paged_attn(const PagedAttnParams& in, const PagedCache& c,
         if (rows && paged_ws(c.B, c.T, c.ng, p.step_ctas, p.chunk_ctas, rows).total <= workspace_bytes) p.stage_rows = rows;
         return launch_paged_chunk(p, s);
     }
+    p.test_wait_ns = test_stall_once();
     EncodeTiledFn enc = nullptr;
     flint_status_t st = get_encoder(&enc);
     if (st != FLINT_OK) return st;

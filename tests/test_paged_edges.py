@@ -32,3 +32,46 @@ def test_falling_boundaries_leave_the_others_right(fa, mn, fp8):  # noqa: F811
     st, out, lse = attend(fa, c, t, max_new=mn)
     assert st == INVALID and torch.equal(out, want) and torch.equal(lse, wl)
     assert append(fa, c, t) == INVALID
+
+
+_TIMEOUT_CHILD = """
+import sys
+sys.path.insert(0, %r)
+import numpy as np
+import torch
+import full_gqa_learned_b200 as fa
+from tests.paged_cases import Case
+from tests.test_paged import append, attend, check_attend
+c = Case([20000], [1], ps=64, seed=42)
+t = c.to("cuda")
+assert append(fa, c, t) == 0
+ws = torch.zeros(fa.paged_workspace_bytes(1, 1, 1, c.table.shape[1], 64, window=0), dtype=torch.uint8, device="cuda")
+# an earlier call's notes: fold the parts of CTAs 0 and 1 into row 0, head 0
+# (status, fold, first and last CTA, second, row, head, rows, pad)
+note = torch.tensor([0, 1, 0, 1, 0, 0, 0, 8, 0], dtype=torch.int32, device="cuda")
+ws[256:256 + 296 * 36].view(torch.int32).view(296, 9).copy_(note.expand(296, 9))
+out = torch.full((1, 4096), 7.0, dtype=torch.bfloat16, device="cuda")
+lse = torch.full((32, 1), 7.0, device="cuda")
+st, _, _ = attend(fa, c, t, out=out, lse=lse, workspace=ws)
+assert st == 4, st                                   # FLINT_ERR_TIMEOUT
+assert (out == 7).all() and (lse == 7).all(), "a stale note was folded"
+st, out, lse = attend(fa, c, t, workspace=ws)        # the hook is one-shot
+assert st == 0
+check_attend(c, t, out, lse)
+print("TIMEOUT_CHILD_OK")
+"""
+
+
+def test_step_wait_that_runs_out_folds_nothing():
+    """A test hook makes the first launch's consumer warps wait 20 ms on a
+    barrier nothing arrives on, so no CTA reaches a pair.  The workspace holds
+    an earlier call's notes (within the call's bounds): the status reads
+    FLINT_ERR_TIMEOUT, nothing is folded, and the next call is right.  In a
+    fresh process, where the hook is read."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _TIMEOUT_CHILD % root], env=dict(os.environ, FLINT_TEST_WAIT_TIMEOUT_MS="20"),
+                       cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "TIMEOUT_CHILD_OK" in r.stdout, r.stdout + r.stderr
