@@ -242,14 +242,15 @@ __host__ __device__ __forceinline__ int paged_new(const PagedCache& c, int max_n
 }
 
 // Joins the sink to a row's running state (M, L in log2 units, O in units of
-// 2^M): the output is O x *scale.
+// 2^M): the output is O x *scale.  A sink that has no log2 in FP32 (infinite, or
+// finite from 2.36e38 on) takes all the weight.
 __device__ __forceinline__ void paged_finish(float M, float L, float sink, float* scale, float* lse) {
-    if (sink == INFINITY) {
+    const float s2 = sink * 1.4426950408889634f;
+    if (s2 == INFINITY) {
         *scale = 0.f;
-        *lse = INFINITY;
+        *lse = sink;
         return;
     }
-    const float s2 = sink * 1.4426950408889634f;
     const float m = fmaxf(M, s2);
     const float a = M > -INFINITY ? exp2f(M - m) : 0.f;
     const float l = L * a + (s2 > -INFINITY ? exp2f(s2 - m) : 0.f);

@@ -75,3 +75,17 @@ def test_step_wait_that_runs_out_folds_nothing():
     r = subprocess.run([sys.executable, "-c", _TIMEOUT_CHILD % root], env=dict(os.environ, FLINT_TEST_WAIT_TIMEOUT_MS="20"),
                        cwd=root, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "TIMEOUT_CHILD_OK" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1, 2], [1, 20]])
+def test_largest_finite_sinks(fa, new, fp8):  # noqa: F811
+    """Sinks whose multiple by log2(e) leaves FP32's range: they take all the
+    weight (output 0, LSE the sink), as the lowest take none."""
+    top = float(np.finfo(np.float32).max)
+    c = Case([300, 70], new, ps=32, fp8=fp8, seed=43, sinks=[top, -top, 2.4e38, -2.4e38, 2.3e38, 0, 1, 2] * 4)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, out, lse = attend(fa, c, t)
+    assert st == 0
+    check_attend(c, t, out, lse, chunk=max(new) > 8)
