@@ -253,9 +253,10 @@ __device__ __forceinline__ void paged_finish(float M, float L, float sink, float
     }
     const float m = fmaxf(M, s2);
     const float a = M > -INFINITY ? exp2f(M - m) : 0.f;
-    const float l = L * a + (s2 > -INFINITY ? exp2f(s2 - m) : 0.f);
-    *scale = l > 0.f ? a / l : 0.f;
-    *lse = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+    const float l = L * a + (s2 == -INFINITY ? 0.f : exp2f(s2 - m));
+    // l == 0: nothing seen and no sink; NaN (of a sink, or of L) goes through
+    *scale = l == 0.f ? 0.f : a / l;
+    *lse = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 // A CTA's share, walked pair by pair.  The pair's place among all W tiles is

@@ -89,3 +89,22 @@ def test_largest_finite_sinks(fa, new, fp8):  # noqa: F811
     st, out, lse = attend(fa, c, t)
     assert st == 0
     check_attend(c, t, out, lse, chunk=max(new) > 8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ctx,new", [(40, [1, 1]), (40, [20, 3]), (9000, [1, 2])])
+def test_nan_reaches_the_lse(fa, ctx, new, fp8):  # noqa: F811
+    """A NaN sink makes its head's outputs and LSE NaN, a NaN key its
+    sequence's and KV head's; no other row's."""
+    c = Case([ctx, 18], new, fp8=fp8, ps=16, seed=47)
+    c.sinks[3] = np.nan
+    t = c.to("cuda")
+    t["k"][0, 1, 5] = float("nan")
+    assert append(fa, c, t) == 0
+    st, out, lse = attend(fa, c, t)
+    assert st == 0
+    want = np.zeros((32, c.T), bool)
+    want[3] = want[8:16, :new[0]] = True
+    assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
+    nan = torch.isnan(out.reshape(c.T, 32, 128)).cpu().numpy()
+    assert np.array_equal(nan.all(-1).T, want) and np.array_equal(nan.any(-1).T, want)
