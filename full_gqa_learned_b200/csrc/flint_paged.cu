@@ -50,7 +50,7 @@ __device__ void paged_check_block(const PagedCache& c, int* status, bool keep_no
     if (threadIdx.x == 0 && (c.cu[0] != 0 || c.cu[c.B] > c.T)) bad = true;
     for (int b = threadIdx.x / per; b < c.B; b += blockDim.x / per) {
         const int a = c.cu[b], n = c.cu[b + 1] - a, L = c.len[b];
-        if (a < 0 || n < 0 || n > c.T || L < 0 || L >= FLINT_MAX_TOKENS) { bad = true; continue; }
+        if (a < 0 || n < 0 || n > c.T || L < 0 || L > FLINT_MAX_TOKENS) { bad = true; continue; }
         if (n == 0) continue;
         const long long end = (long long)L + n;
         if (end > FLINT_MAX_TOKENS || end > ((long long)c.max_pages << c.ps_log2)) { bad = true; continue; }

@@ -234,7 +234,7 @@ __host__ __device__ inline PagedWs paged_ws(int B, int T, int ng, int step_ctas,
 // New tokens of the sequence whose packed rows are [a, z) at positions len ..;
 // -1 where its entries are ill-formed.
 __host__ __device__ __forceinline__ int paged_new(const PagedCache& c, int max_new, int a, int z, int len) {
-    if (a < 0 || z < a || z > c.T || len < 0 || len >= FLINT_MAX_TOKENS) return -1;
+    if (a < 0 || z < a || z > c.T || len < 0 || len > FLINT_MAX_TOKENS) return -1;
     const int n = z - a;
     const long long end = (long long)len + n;
     if (n > max_new) return -1;

@@ -379,7 +379,8 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  *             with a <= 448 x 2^e (keys: [-24, 7], so that they fit FP16);
  *             larger values saturate.
  *  page_table int32 [B, max_pages].
- *  cache_len  int32 [B]: positions cached before this call's new tokens.
+ *  cache_len  int32 [B]: positions cached before this call's new tokens, 0 to
+ *             FLINT_MAX_TOKENS.
  *  cu_new     int32 [B+1]: new token t, cu_new[b] <= t < cu_new[b+1], belongs
  *             to sequence b and sits at position cache_len[b] + t - cu_new[b].
  *             cu_new[0] = 0, non-decreasing, cu_new[B] <= T.  A sequence may

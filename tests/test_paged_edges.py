@@ -92,6 +92,30 @@ def test_largest_finite_sinks(fa, new, fp8):  # noqa: F811
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_a_full_sequence_may_idle(fa, fp8):  # noqa: F811
+    """A sequence at the most positions there can be, without new tokens, is
+    no error: no position of it is past the limit."""
+    c = Case([40, 7, 3], [2, 0, 1], ps=16, fp8=fp8, seed=44)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    want = {mn: attend(fa, c, t, max_new=mn)[1:] for mn in (2, 64)}
+    at, cu = torch.tensor([3, 0, 1], dtype=torch.int32, device="cuda"), torch.tensor([0, 20, 20, 22], dtype=torch.int32, device="cuda")
+    sc = dict(k_scales=t["k_scales"], v_scales=t["v_scales"])
+    kv = fa.paged_read(t["k_pages"], t["v_pages"], t["table"], at, cu, 22, **sc)
+    t["ctx"][1] = at[1] = 1 << 24
+    assert append(fa, c, t) == 0
+    for mn, (o, l) in want.items():
+        st, out, lse = attend(fa, c, t, max_new=mn)
+        assert st == 0 and torch.equal(out, o) and torch.equal(lse, l)
+    k2, v2 = fa.paged_read(t["k_pages"], t["v_pages"], t["table"], at, cu, 22, **sc)
+    assert fa.device_status(fa.paged_read.last_workspace) == 0 and torch.equal(kv[0], k2) and torch.equal(kv[1], v2)
+    t["ctx"][1] = (1 << 24) + 1                           # past the limit it is one
+    assert append(fa, c, t) == INVALID
+    for mn in want:
+        assert attend(fa, c, t, max_new=mn)[0] == INVALID
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("ctx,new", [(40, [1, 1]), (40, [20, 3]), (9000, [1, 2])])
 def test_nan_reaches_the_lse(fa, ctx, new, fp8):  # noqa: F811
     """A NaN sink makes its head's outputs and LSE NaN, a NaN key its
