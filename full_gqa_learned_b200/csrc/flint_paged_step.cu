@@ -48,8 +48,11 @@
 // * q~ is FP16, as in the forward; P for BF16 values is split into high and
 //   low parts (both multiplied), so its rounding does not show.  8-bit
 //   values: the codes are exact in FP16 and the scale 2^e joins the exponent,
-//   p' = 2^(z + e - m), with m the maximum of z + e, while l sums
-//   p' 2^-e; P' carries FP16's 11 bits where its product matters.
+//   p' = 2^(z + e - m + 7), with m the running maximum of z + e, while l sums
+//   p' 2^-e.  The 7 put the largest P' at 2^15, the top of FP16 (the lazy
+//   maximum may be passed by 2^8): it keeps 11 bits down to 2^-21 of the
+//   largest term, and what is less is off by 2^-32 of it at most, so that
+//   tokens far below one with a large value scale still count.
 // Every wait is bounded (FLINT_ERR_TIMEOUT in the status word).
 //
 // Measured: one token each of 2 sequences over 100,003 to 131,071 positions,
@@ -83,6 +86,8 @@ constexpr uint32_t kStepStages = 3;
 constexpr uint32_t kStepHalf = 16384;                    // a tile's keys, or values
 constexpr uint32_t kStepStage = 2 * kStepHalf;
 constexpr int kStepCtasPerSm = 2;
+// Scores of 8-bit values are held 2^7 above the running maximum's unit.
+template <bool FP8> constexpr float kStepLift = FP8 ? 7.f : 0.f;
 
 // Positions of a warp's block and of a tile; 16-position pieces of a tile.
 template <bool FP8> struct StepTile {
@@ -607,7 +612,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float mm = m[nt][e & 1];
-                        pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm : 0.f));
+                        pr[e] = st_ex2(s[u][nt][e] - (mm > -INFINITY ? mm - kStepLift<FP8> : 0.f));
                     }
                     if constexpr (!FP8) {
                         l[nt][0] += pr[0] + pr[2];
@@ -682,6 +687,7 @@ paged_step_kernel(const __grid_constant__ StepMaps maps, const PagedAttnParams p
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], o);
+                m[nt][h] -= kStepLift<FP8>;                // l and acc are in units of 2^m again
                 if (j == 0) {
                     s_m[warp * S::rows + nt * kGroup + 2 * i + h] = m[nt][h];
                     s_l[warp * S::rows + nt * kGroup + 2 * i + h] = l[nt][h];

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.paged_cases import Case
+from oracle import paged as OP
+from tests.paged_cases import Case, values
 from tests.test_paged import append, attend, check_attend, fa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -113,6 +114,62 @@ def test_a_full_sequence_may_idle(fa, fp8):  # noqa: F811
     assert append(fa, c, t) == INVALID
     for mn in want:
         assert attend(fa, c, t, max_new=mn)[0] == INVALID
+
+
+@pytest.mark.parametrize("new", [1, 2])
+def test_value_scales_far_apart_on_8_bit_pages(fa, new):  # noqa: F811
+    """One cached token with a weight and a value scale far above the others',
+    and values in one channel only: what the others leave in the remaining
+    channels is small beside it but not lost.
+
+    The kernel multiplies P' = p 2^e in FP16, in units 2^(m - 7) with m at most
+    the largest log2(p 2^e) of the row: a term is rounded to 2^-11 of itself, or
+    by at most 2^-25 x 2^(m - 7), which a code of at most 448 < 2^9 multiplies.
+    So the N positions add at most N 2^-23 max_j p_j 2^(e_j) to the usual
+    tolerance."""
+    B, ctx, g = 24, 300, 2
+    c = Case([ctx] * B, [new] * B, ps=16, fp8=True, g=g, seed=45, sinks=[-np.inf] * 16)
+    r = np.random.default_rng(46)
+    one = r.standard_normal(128)
+    c.q = torch.from_numpy(np.broadcast_to(one.astype(np.float32), (c.T, 8 * g, 128)).copy()).bfloat16()
+    qt = OP.norm_rope(c.q[0, 0].double().numpy(), c.wq, 0, False)
+    kv = [x.float() for x in (c.k_pages, c.v_pages)]
+    ks, vs = (x.view(torch.uint8).clone() for x in (c.k_scales, c.v_scales))
+    for b in range(B):
+        for p in range(ctx):
+            page, slot = c.table[b, p // 16], p % 16
+            k, v = np.zeros((g, 128)), 1.0 + 0.5 * np.abs(r.standard_normal((g, 128)))
+            if p == 37:
+                k[:] = qt * (0.2 + 0.05 * b)              # logits of 2.3 to 16
+                v[:], v[:, 5] = 0, 2.0 ** 7
+            for x, s, y, most in ((kv[0], ks, k, 7), (kv[1], vs, v, 40)):
+                code, e = OP.quantise(y, most)
+                x[page, :, slot], s[page, :, slot] = torch.from_numpy(code).float(), torch.from_numpy(e + 127).to(torch.uint8)
+    c.k_pages, c.v_pages = (x.to(torch.float8_e4m3fn) for x in kv)
+    c.k_scales, c.v_scales = (x.view(torch.float8_e8m0fnu) for x in (ks, vs))
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, out, lse = attend(fa, c, t)
+    assert st == 0
+    K, V = values(t["k_pages"], t["k_scales"]), values(t["v_pages"], t["v_scales"])
+    E = np.exp2(t["v_scales"].cpu().view(torch.uint8).double().numpy() - 127)
+    args = (c.q.double().numpy(), c.wq, c.sinks, K, V, c.table, c.ctx, c.cu)
+    ref, rl, ab, spread = OP.attn(*args, window=0, use_rope=False)
+    dz = (2.0 ** -11 * spread + 2e-5)[..., None]
+    # max_j p_j 2^(e_j) / Z of a row
+    top = np.zeros((c.T, 8 * g, 1))
+    for i in range(c.T):
+        b, p = i // new, ctx + i % new
+        j = np.arange(p + 1)
+        page = c.table[b][j // 16]
+        for h in range(8 * g):
+            z = K[page, h // 8, j % 16] @ OP.norm_rope(c.q[i, h].double().numpy(), c.wq, p, False) / np.sqrt(128.0)
+            top[i, h] = (np.exp(z - rl[h, i]) * E[page, h // 8, j % 16]).max()
+    tol = 2.0 ** -8 * np.abs(ref) + (2 * dz + 2.0 ** -15 + 2.0 ** -11) * ab + (ctx + new) * 2.0 ** -23 * top
+    err = np.abs(out.float().cpu().numpy().reshape(ref.shape) - ref)
+    rel = np.delete(err / np.abs(ref), 5, -1)
+    print("largest error relative to the output, other channels: %.3e" % rel.max())
+    assert (err <= tol).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
