@@ -189,3 +189,17 @@ def test_nan_reaches_the_lse(fa, ctx, new, fp8):  # noqa: F811
     assert np.array_equal(torch.isnan(lse).cpu().numpy(), want)
     nan = torch.isnan(out.reshape(c.T, 32, 128)).cpu().numpy()
     assert np.array_equal(nan.all(-1).T, want) and np.array_equal(nan.any(-1).T, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new", [[1, 2], [33, 100]])
+def test_a_window_larger_than_any_position(fa, new, fp8):  # noqa: F811
+    """The largest window there is sees what no window does."""
+    c = Case([300, 90], new, ps=16, fp8=fp8, seed=48)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, want, wl = attend(fa, c, t)
+    assert st == 0
+    c.window = 2 ** 31 - 1
+    st, out, lse = attend(fa, c, t)
+    assert st == 0 and torch.equal(out, want) and torch.equal(lse, wl)
