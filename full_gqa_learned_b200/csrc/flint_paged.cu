@@ -10,7 +10,8 @@
 // holds them) with a <= 448 x 2^e (448: the largest E4M3 number), the codes are
 // E4M3(x 2^-e).  A power of two makes
 // the scaling exact, so the code's rounding (half a step, 2^-4 relative) is
-// the only one, and what is read back is exact in FP16 or BF16.  An arbitrary
+// the only one, and what is read back is exact in BF16, and in FP16 from a scale
+// of 2^-15 on.  An arbitrary
 // scale would not round better: E4M3 is a floating format.
 //
 // Both kernels move bytes: 512 read and 512 or 258 written per token and head
@@ -96,7 +97,8 @@ __device__ __forceinline__ PagedPlace paged_locate(const PagedCache& c, int t0, 
 }
 
 // Tokens a warp takes: eight on long calls, so that one look-up serves many
-// rows; fewer where a call of few tokens would leave SMs idle.  Measured:
+// rows; fewer where a call of few tokens would leave SMs idle.  Measured on four
+// heads (fewer heads take the same tokens, so fewer rows, a warp):
 // appending 78,523 tokens to 8-bit (16-bit) pages 49 us (55), with 16 tokens a warp
 // 55 (59).
 __host__ __device__ inline int paged_tokens_per_warp(int T) { return T >= 16384 ? 8 : T >= 4096 ? 4 : T >= 2048 ? 2 : 1; }

@@ -1,6 +1,7 @@
 // Definitions shared by the kernels of the paged key/value cache
-// (flint_paged.cu: append, read back, the plan of an attention call and the
-// host side; flint_paged_step.cu: attention of few new tokens per sequence).
+// (flint_paged.cu: append, read back and the host side; flint_paged_step.cu with
+// flint_paged_walk.cuh: attention of few new tokens per sequence;
+// flint_paged_chunk.cu: of many).
 //
 // Position p of sequence b lives in page table[b][p / ps], slot p mod ps, of
 // pools laid out [num_pages, ng, ps, 128] (ng KV heads, ps slots a page), so
@@ -259,8 +260,7 @@ __device__ __forceinline__ void paged_finish(float M, float L, float sink, float
     *lse = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
-// A CTA's share, walked pair by pair.  The pair's place among all W tiles is
-// needed only where it is held in part (paged_seg_begin).
+// A chunk CTA's share, walked pair by pair.
 struct PagedShare {
     int gi, head, off;           // the next pair; off: tile of it that the share enters at
     int left;                    // tiles left in the share

@@ -19,8 +19,9 @@
 //   rows that hold no position of the group (stale slots may hold NaN, and
 //   0 x NaN would reach every row); masked columns of S need no such care.
 // * 8-bit pages: where the workspace has room, a kernel in front expands the
-//   positions the call reads (codes x 2^e: K in FP16, V in BF16, both exact)
-//   into rows of their own, loaded like pages of any size.  Otherwise a third
+//   positions the call reads (codes x 2^e: V in BF16, exact; K in FP16, exact from
+//   e = -15 on, below that rounded to FP16's subnormals) into rows of their own,
+//   loaded like pages of any size.  Otherwise a third
 //   warpgroup does the same chunk by chunk, into the swizzled layout that the
 //   tensor core reads; it does so again for every group of 32 tokens, and four
 //   warps need 5 to 7 us a chunk where the products and the softmax take 3 to 4
@@ -29,11 +30,16 @@
 // * Warp 1 issues S = Q K^T and O += P V per chunk and tile; warps 4-7 and
 //   8-11 are the softmax warpgroups of the two tiles (one thread a row): RMS
 //   norm and rotation of the queries in place as FP16 when a tile lands, then
-//   the online softmax, P in BF16 over S in tensor memory.  The two tiles
+//   the online softmax, P in BF16 over S in tensor memory (the product wants
+//   P in V's type, and V in BF16 holds what FP16's range does not; a second, low
+//   part of P would double the products, for an output that BF16 rounds by as
+//   much: 2.4e-3 from the exact one instead of 1.7e-3).  The two tiles
 //   alternate, so one's softmax runs under the other's products.  Interior
 //   chunks after the first skip the row max while the row sum of their terms
 //   stays within 2^8.  A group of at most 16 rows runs on one tile alone.
 // Every wait is bounded (FLINT_ERR_TIMEOUT in the status word, abort, drain).
+// The softmax warps spill 244 to 460 bytes a thread (stores; on-chip conversion
+// most); states kept elsewhere were slower.
 //
 // Measured: 2,048 tokens over 32,049 positions, 16-bit pages: 1,179 us, 883 TF/s,
 // 0.53 of the measured bf16 rate, as the forward kernel (its softmax and tensor
@@ -606,8 +612,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int kk = 1; kk < 8; ++kk)
                 if (kk < nk) mma_ts_w(d, pa + 8u * kk, vb + kk * (2048 >> 4), v_hi, idesc_pv, 1u);
         };
-        // the share is walked by the whole warp (its search is warp-wide);
-        // lane 0 waits and issues, the others follow its outcome
+        // the whole warp walks the share; lane 0 waits and issues, the others
+        // follow its outcome
         uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qrph[2] = {0u, 0u}, pph[2] = {0u, 0u};
         bool ok = true;
         while (ok && paged_share_next(share, groups, ng, sg)) {

@@ -385,7 +385,8 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  *             to sequence b and sits at position cache_len[b] + t - cu_new[b].
  *             cu_new[0] = 0, non-decreasing, cu_new[B] <= T.  A sequence may
  *             have no new token.  Rows from cu_new[B] on belong to nobody:
- *             they are not read, and output rows there are left as they were.
+ *             they may hold anything, and output rows there are left as they
+ *             were.
  *  B          sequences, 0 <= B <= FLINT_MAX_DECODE_BATCH;  T  rows of the
  *             packed tensors, 0 <= T <= FLINT_MAX_TOKENS.  B == 0 or T == 0:
  *             no-op.
@@ -397,7 +398,7 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  *             ill-formed cu_new or cache_len, a position past
  *             max_pages x page_size or FLINT_MAX_TOKENS, or a page the call
  *             needs that is outside [0, num_pages).  Such sequences' results
- *             are undefined; nothing outside the pools is accessed.
+ *             are undefined; nothing outside the call's arrays is accessed.
  */
 #define FLINT_PAGED_STATUS_BYTES 256
 
@@ -410,7 +411,8 @@ FLINT_API flint_status_t flint_attn_decode(const void* q, const void* k, const v
  * A page table entry of -1 drops the token (a sliding layer keeps no page
  * for positions that no later token sees).  A slot that several tokens of one
  * call name (a page listed twice) ends up undefined.
- * Infinite elements saturate in 8-bit pages; NaN stays NaN.
+ * Infinite values saturate in 8-bit pages; NaN stays NaN, and an infinite key,
+ * which has no norm, becomes NaN.
  */
 FLINT_API flint_status_t flint_paged_append(const void* k, const void* v, const float* k_norm_w,
                               void* k_pages, void* v_pages, void* k_scales, void* v_scales,
@@ -452,14 +454,24 @@ FLINT_API flint_status_t flint_paged_read(const void* k_pages, const void* v_pag
  *             Neither may overlap an input.
  *  workspace  flint_attn_paged_workspace_bytes(...) bytes; not shared by
  *             calls that may overlap on the GPU.  For 8-bit pages and max_new
- *             > 8 that counts room (up to 512 MiB, else none) to expand the
- *             positions the call reads to 16 bits first; a workspace of the
- *             size for 16-bit pages (eight_bit == 0) is accepted, too: the
- *             call then converts on chip, with the same result, in 1.2 times
- *             (few tokens a sequence) to twice the time.
+ *             > 8 that counts room to expand the positions the call reads to 16
+ *             bits first: for each sequence its window, without one all of
+ *             max_pages x page_size (a table cut to the longest sequence keeps
+ *             it small), but none where B of those pass 512 MiB.  A workspace
+ *             of the size for 16-bit pages (eight_bit == 0) is accepted, too.
+ *             Without the room the call converts on chip, with the same
+ *             result, in 1.2 times (few tokens a sequence) to twice the time.
  * Cached values and keys at positions a token sees must be finite, keys within
- * FP16's range, and scales within 2^-24 .. 2^40; slots of other positions may hold anything, and page
- * table entries that no new token's window touches are not read.
+ * FP16's range, keys' scales within 2^-24 .. 2^7 and values' within 2^-24 ..
+ * 2^40; slots of other positions may hold anything, and page table entries that
+ * no new token's window touches are not read.
+ * Roundings: normalised queries are FP16.  max_new <= 8: the weights keep 16
+ * bits (16-bit pages) or 11 (8-bit pages; terms below 2^-21 of a row's largest
+ * weight x value scale keep fewer, to 2^-32 of it).  max_new > 8: the weights
+ * are BF16, as in flint_attn_fwd, and 8-bit keys with a scale below 2^-15 are
+ * rounded to FP16's subnormals.  So a token's output differs in its last BF16
+ * place with what else is in the call (2.4e-3 from the exact one, relative,
+ * against 1.7e-3).
  * Results do not depend on timing: every sum has a fixed order.
  */
 FLINT_API size_t flint_attn_paged_workspace_bytes(int32_t B, int32_t T, int32_t max_new,

@@ -8,7 +8,7 @@ import torch
 
 from oracle import paged as OP
 from tests.paged_cases import Case, values
-from tests.test_paged import append, attend, check_attend, fa  # noqa: F401
+from tests.test_paged import append, attend, check_append, check_attend, fa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 INVALID = 1
@@ -203,3 +203,28 @@ def test_a_window_larger_than_any_position(fa, new, fp8):  # noqa: F811
     c.window = 2 ** 31 - 1
     st, out, lse = attend(fa, c, t)
     assert st == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ctx,new", [([40, 18, 300], [1, 1, 1]), ([40, 18, 300], [2, 1, 3]), ([700, 18, 0], [40, 5, 20]), ([9000, 18], [2, 1])])
+def test_nan_queries_stay_in_their_rows(fa, ctx, new, fp8):  # noqa: F811
+    """NaN in a token's query, and in the rows behind the last sequence,
+    reaches no other row, of the same tile or group either."""
+    c = Case(ctx, new, fp8=fp8, ps=16, seed=49, extra=9)
+    t = c.to("cuda")
+    row = new[0] - 1
+    t["q"][row, 9] = t["q"][c.rows:] = t["k"][c.rows:] = t["v"][c.rows:] = float("nan")
+    assert append(fa, c, t) == 0
+    check_append(c, t)
+    out, lse = torch.full((c.T, 4096), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((32, c.T), 7.0, device="cuda")
+    st, out, lse = attend(fa, c, t, out=out, lse=lse)
+    assert st == 0 and (out[c.rows:] == 7).all() and (lse[:, c.rows:] == 7).all()
+    o = out.reshape(c.T, 32, 128)
+    assert torch.isnan(o[row, 9]).all() and torch.isnan(lse[9, row])
+    # in the place of the NaN head: the oracle's own, so that the rest is compared
+    t["q"] = torch.where(torch.isnan(t["q"]), 0, t["q"])
+    st, ref, rl = attend(fa, c, t)
+    assert st == 0
+    c.q[row, 9], c.q[c.rows:] = 0, 0
+    o[row, 9], lse[9, row] = ref.reshape(c.T, 32, 128)[row, 9], rl[9, row]
+    check_attend(c, t, out, lse, chunk=max(new) > 8)
