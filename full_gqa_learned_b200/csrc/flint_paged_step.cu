@@ -56,7 +56,7 @@
 // Every wait is bounded (FLINT_ERR_TIMEOUT in the status word).
 //
 // Measured: one token each of 2 sequences over 100,003 to 131,071 positions,
-// 16-bit pages: 75 us for 450 MB, 6.0 TB/s, 0.91 of the measured copy rate (82 us
+// 16-bit pages: 75 to 77 us for 450 MB, 6.0 TB/s, 0.91 of the measured copy rate (82 us
 // with both launches); 128 sequences at a window of 513 37 us for 137 MB; 64
 // sequences of up to 4,096 on 8-bit pages 40 us for 112 MB.  About 11 us of a
 // call are its start (launch, lengths, page table, first tile) and the fold.
