@@ -228,3 +228,27 @@ def test_nan_queries_stay_in_their_rows(fa, ctx, new, fp8):  # noqa: F811
     c.q[row, 9], c.q[c.rows:] = 0, 0
     o[row, 9], lse[9, row] = ref.reshape(c.T, 32, 128)[row, 9], rl[9, row]
     check_attend(c, t, out, lse, chunk=max(new) > 8)
+
+
+@pytest.mark.parametrize("where", ["length", "fall"])
+def test_one_ill_formed_sequence_among_the_most(fa, where):  # noqa: F811
+    """As many sequences as a call may have, most of them idle: the call with
+    an ill-formed one walks all of them and still ends with the others' rows
+    as they are without it."""
+    B = 65535
+    r = np.random.default_rng(50)
+    ctx, new = np.zeros(B, int), np.zeros(B, int)
+    live = np.sort(r.choice(B - 2, 60, replace=False))
+    ctx[live], new[live] = r.integers(0, 3000, 60), r.integers(1, 3, 60)
+    c = Case(ctx.tolist(), new.tolist(), g=1, ps=128, seed=51)
+    t = c.to("cuda")
+    assert append(fa, c, t) == 0
+    st, want, wl = attend(fa, c, t, max_new=2)
+    assert st == 0
+    check_attend(c, t, want, wl)
+    if where == "length":
+        t["ctx"][B - 2] = -1
+    else:
+        t["cu"][B - 1] = 0                                # falls at an idle sequence, and rises for the next one
+    st, out, lse = attend(fa, c, t, max_new=2)
+    assert st == INVALID and torch.equal(out, want) and torch.equal(lse, wl)
